@@ -31,6 +31,7 @@ STATUS = {0: "FA_OK", 1: "FA_ERR_INVALID_ARG", 2: "FA_ERR_UNSUPPORTED", 3: "FA_E
 
 # Every symbol include/fa.h declares, with its ctypes signature.
 _vp, _i, _f, _sz, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_uint64
+_i64 = ctypes.c_int64
 SIGNATURES = {
     "fa_fwd": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _f, _vp, _vp, _vp]),
     "fa_bwd_workspace_size": (_sz, [_i, _i, _i, _i]),
@@ -48,6 +49,10 @@ SIGNATURES = {
                            _vp, _vp, _sz, _vp]),
     "fa_decode_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_decode": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _sz, _vp]),
+    "fa_paged_append": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp]),
+    "fa_paged_decode_workspace_size": (_sz, [_i, _i, _i, _i, _i64, _i]),
+    "fa_paged_decode": (_i, [_vp, _vp, _i, _vp, _f, _vp, _i64, _i64, _i, _vp, _vp, _vp, _sz, _vp]),
+    "fa_paged_evict": (_i, [_vp, _vp, _vp, _i64, _i, _vp, _i64, _i64, _i, _i, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
     "fa_standard_fwd_workspace_size": (_sz, [_i, _i, _i, _i]),
     "fa_standard_fwd": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _f, _vp, _vp, _vp, _sz, _vp]),
     "fa_bwd_static_workspace": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _f, _vp, _vp,
@@ -58,6 +63,18 @@ SIGNATURES = {
     "fa_selftest_bounded_wait": (_i, [_u64, _vp]),
     "fa_selftest_mma_tile": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp]),
 }
+
+
+class _Rows(ctypes.Structure):
+    """fa_rows of include/fa.h."""
+    _fields_ = [("data", _vp), ("row_stride", _i64), ("head_stride", _i64)]
+
+
+class _PagedCache(ctypes.Structure):
+    """fa_paged_cache of include/fa.h."""
+    _fields_ = [("K", _vp), ("V", _vp), ("dtype", _i), ("num_pages", _i), ("page_size", _i), ("Hkv", _i), ("d", _i),
+                ("page_stride", _i64), ("head_stride", _i64), ("row_stride", _i64), ("k_scale", _vp),
+                ("v_scale", _vp), ("page_table", _vp), ("B", _i), ("max_pages", _i), ("table_stride", _i64)]
 
 
 class FAError(RuntimeError):
@@ -307,6 +324,180 @@ def decode(Q, K, V, mask="none", scale=None, O=None, LSE=None, workspace=None, s
     _check(lib().fa_decode(Q.data_ptr(), K.data_ptr(), V.data_ptr(), B, H, N, Nk, d, kind, scale, O.data_ptr(),
                            LSE.data_ptr(), wptr, wbytes, _stream(stream)), "fa_decode")
     return O, LSE
+
+
+# ---- packed rows and the paged cache -----------------------------------------
+def _run(name, device, stream, *args):
+    """Call ``name`` with ``device`` current (its kernels launch there) on
+    ``stream``, by default that device's current stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _check(getattr(lib(), name)(*args, _stream(stream)), name)
+    _check(getattr(lib(), name)(*args, _stream(stream)), name)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new buffer for a call on ``stream``: the allocator hands memory out in
+    the order of the stream it is asked on, so that must be the call's."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t, name, heads=None, d=None, rows=None, device=None):
+    """fa_rows of a bf16 CUDA tensor [rows, heads, d] whose last dimension is
+    contiguous; the rows and heads may be strided."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 3):
+        raise FAError(1, f"{name} must be a bf16 CUDA tensor [rows, heads, d]")
+    n, h, w = t.shape
+    if (heads is not None and h != heads) or (d is not None and w != d) or (rows is not None and n != rows):
+        raise FAError(1, f"{name} must be [{'rows' if rows is None else rows}, {'heads' if heads is None else heads}, "
+                         f"{'d' if d is None else d}], got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise FAError(1, f"{name} must be on {device}, got {t.device}")
+    rs, hs, ds = t.stride()
+    rs, hs = rs if n > 1 else h * w, hs if h > 1 else w  # the stride of a single row or head is never used
+    if (ds != 1 and w > 1) or rs % 8 or hs % 8 or t.data_ptr() % 16:
+        raise FAError(1, f"{name}: d must be contiguous, and rows and heads start on 16-byte boundaries (strides "
+                         f"{t.stride()})")
+    return _Rows(t.data_ptr(), rs, hs)
+
+
+def _int32(t, name, n, device):
+    """Device pointer of a contiguous int32 vector [n]."""
+    if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype == torch.int32 and t.dim() == 1
+            and t.is_contiguous() and t.shape[0] == n):
+        raise FAError(1, f"{name} must be a contiguous int32 tensor [{n}] on {device}")
+    return t.data_ptr()
+
+
+def _table(t, name, device):
+    """Pointer, width and row stride of a page table [B, pages] (int32)."""
+    if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype == torch.int32 and t.dim() == 2
+            and t.shape[0] > 0 and t.shape[1] > 0 and (t.stride(1) == 1 or t.shape[1] == 1)):
+        raise FAError(1, f"{name} must be an int32 tensor [B, pages] on {device} with contiguous rows")
+    return t.data_ptr(), t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _paged_cache(k_cache, v_cache, page_table, k_scale=None, v_scale=None, scales=True):
+    """fa_paged_cache of two pools [pages, Hkv, page_size, d]."""
+    for t in (k_cache, v_cache):
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4
+                and t.dtype in (torch.bfloat16, torch.float8_e4m3fn)):
+            raise FAError(1, "cache pools must be bf16 or float8_e4m3fn CUDA tensors [pages, Hkv, page_size, d]")
+    dev = k_cache.device
+    if (k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or v_cache.device != dev
+            or k_cache.stride() != v_cache.stride()):
+        raise FAError(1, "the K and V pools must have one shape, type, device and layout")
+    pages, Hkv, page, d = k_cache.shape
+    eight = k_cache.dtype == torch.float8_e4m3fn
+    unit = 16 if eight else 8
+    sp, sh, sr, sd = k_cache.stride()
+    # (the stride of a dimension of one entry is never used)
+    sp, sh, sr = sp if pages > 1 else 0, sh if Hkv > 1 else 0, sr if page > 1 else 0
+    if (sd != 1 and d > 1) or sp % unit or sh % unit or sr % unit or k_cache.data_ptr() % 16 or v_cache.data_ptr() % 16:
+        raise FAError(1, "cache rows must be contiguous and start on 16-byte boundaries")
+    ks = vs = None
+    if eight and scales:
+        ks = _check_buf(k_scale, "k_scale", (Hkv,), torch.float32, dev).data_ptr()
+        vs = _check_buf(v_scale, "v_scale", (Hkv,), torch.float32, dev).data_ptr()
+    elif k_scale is not None or v_scale is not None:
+        raise FAError(1, "k_scale and v_scale belong to float8_e4m3fn pools")
+    tp, width, ts = _table(page_table, "page_table", dev)
+    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), 1 if eight else 0, pages, page, Hkv, d, sp, sh, sr, ks,
+                       vs, tp, page_table.shape[0], width, ts)
+
+
+def _weights(t, name, B, Hkv, least, device):
+    """Pointer and strides of fp32 weights [B, Hkv, >= least]."""
+    if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype == torch.float32 and t.dim() == 3
+            and tuple(t.shape[:2]) == (B, Hkv) and t.shape[2] >= least and (t.stride(2) == 1 or t.shape[2] == 1)):
+        raise FAError(1, f"{name} must be an fp32 tensor [{B}, {Hkv}, at least {least}] on {device} with contiguous rows")
+    return t.data_ptr(), t.stride(0) if B > 1 else 0, t.stride(1) if Hkv > 1 else 0
+
+
+def paged_append(K, V, cu_seqlens, lens, k_cache, v_cache, page_table, k_scale=None, v_scale=None, stream=None):
+    """Write the packed rows K, V [T, Hkv, d] (bf16) into the paged cache: row
+    t of sequence b (cu_seqlens[b] <= t < cu_seqlens[b + 1], int32 [B + 1])
+    goes to position lens[b] + t - cu_seqlens[b]; ``lens`` (int32 [B]) counts
+    the positions already held and is not changed.  Pools are
+    [pages, Hkv, page_size, d], bf16 or float8_e4m3fn (then with fp32 scales
+    [Hkv]); page_table is int32 [B, pages]."""
+    c = _paged_cache(k_cache, v_cache, page_table, k_scale, v_scale)
+    dev = k_cache.device
+    k = _rows(K, "K", c.Hkv, c.d, device=dev)
+    v = _rows(V, "V", c.Hkv, c.d, K.shape[0], dev)
+    _run("fa_paged_append", dev, stream, ctypes.byref(c), ctypes.byref(k), ctypes.byref(v),
+         _int32(cu_seqlens, "cu_seqlens", c.B + 1, dev), _int32(lens, "lens", c.B, dev), K.shape[0])
+
+
+def paged_decode_workspace_size(B, Hq, Hkv, d, max_len, weights=False) -> int:
+    """Bytes for ``paged_decode``; max_len is the page table's width times the
+    page size."""
+    return int(lib().fa_paged_decode_workspace_size(B, Hq, Hkv, d, max_len, 1 if weights else 0))
+
+
+def paged_decode(Q, k_cache, v_cache, page_table, lens, scale=None, k_scale=None, v_scale=None, weights=None,
+                 accumulate=False, O=None, LSE=None, workspace=None, stream=None):
+    """One new token per sequence over its cached keys, grouped heads: Q
+    [B, Hq, d] bf16 against the first lens[b] positions of the paged cache;
+    returns O [B, Hq, d] bf16 and LSE [B, Hq] fp32.  ``weights`` (fp32
+    [B, Hkv, at least pages * page_size]) receives the attention that each key
+    drew, summed over its group of query heads, or is raised by it with
+    ``accumulate``."""
+    c = _paged_cache(k_cache, v_cache, page_table, k_scale, v_scale)
+    dev, B, d = k_cache.device, c.B, c.d
+    q = _rows(Q, "Q", None, d, B, dev)
+    Hq = Q.shape[1]
+    cap = c.max_pages * c.page_size
+    scale = d ** -0.5 if scale is None else float(scale)
+    lp = _int32(lens, "lens", B, dev)
+    wp = wb = wh = 0
+    if weights is not None:
+        wp, wb, wh = _weights(weights, "weights", B, c.Hkv, cap, dev)
+    O = _empty((B, Hq, d), torch.bfloat16, dev, stream) if O is None else \
+        _check_buf(O, "O", (B, Hq, d), torch.bfloat16, dev)
+    LSE = _empty((B, Hq), torch.float32, dev, stream) if LSE is None else \
+        _check_buf(LSE, "LSE", (B, Hq), torch.float32, dev)
+    need = paged_decode_workspace_size(B, Hq, c.Hkv, d, cap, weights is not None)
+    if workspace is None:
+        workspace = _empty(need, torch.uint8, dev, stream)
+    sp, sn = _workspace(workspace, need, dev)
+    _run("fa_paged_decode", dev, stream, ctypes.byref(c), ctypes.byref(q), Hq, lp, scale, wp or None, wb, wh,
+         1 if accumulate else 0, O.data_ptr(), LSE.data_ptr(), sp, sn)
+    return O, LSE
+
+
+def paged_evict(weights, k_cache, v_cache, page_table, lens, table_out, budget, recent, weights_out, kept=None,
+                lens_out=None, stream=None):
+    """Cut each sequence's cache to ``budget`` rows a head: the last ``recent``
+    and the others of largest weight, copied in order to the pages of
+    ``table_out`` (int32 [B, pages], pages of the same pools that no sequence
+    of the call reads).  Returns kept [B, Hkv, budget] int32 (the positions
+    kept, then -1) and lens_out [B] int32; ``weights_out`` (fp32
+    [B, Hkv, width]) gets the kept rows' weights, then zeros."""
+    c = _paged_cache(k_cache, v_cache, page_table, scales=False)  # 8-bit rows move as they are
+    dev, B, Hkv = k_cache.device, c.B, c.Hkv
+    cap = c.max_pages * c.page_size
+    wp, wb, wh = _weights(weights, "weights", B, Hkv, cap, dev)
+    op, ob, oh = _weights(weights_out, "weights_out", B, Hkv, min(int(budget), cap), dev)
+    tp, width, ts = _table(table_out, "table_out", dev)
+    if table_out.shape[0] != B:
+        raise FAError(1, f"table_out must have {B} rows")
+    lp = _int32(lens, "lens", B, dev)
+    budget, recent = int(budget), int(recent)
+    if budget <= 0 or not 0 <= recent <= budget:
+        raise FAError(1, "paged_evict takes budget > 0 and 0 <= recent <= budget")
+    kept = _empty((B, Hkv, budget), torch.int32, dev, stream) if kept is None else \
+        _check_buf(kept, "kept", (B, Hkv, budget), torch.int32, dev)
+    lens_out = _empty((B,), torch.int32, dev, stream) if lens_out is None else \
+        _check_buf(lens_out, "lens_out", (B,), torch.int32, dev)
+    _run("fa_paged_evict", dev, stream, ctypes.byref(c), lp, tp, ts, width, wp, wb, wh, budget, recent, op, ob, oh,
+         weights_out.shape[2], kept.data_ptr(), lens_out.data_ptr())
+    return kept, lens_out
 
 
 def standard_fwd(Q, K, V, mask="none", block_mask=None, scale=None, O=None, LSE=None, workspace=None,

@@ -276,6 +276,108 @@ fa_status fa_standard_fwd(const void* Q, const void* K, const void* V, int B, in
   return launch_standard_fwd(p, Q, K, V, O, LSE, workspace, (cudaStream_t)stream);
 }
 
+// ---- paged cache ----
+static bool valid_rows(const fa_rows* r, int d) {
+  return r && r->data && aligned(r->data, 16) && r->row_stride >= 0 && r->head_stride >= 0 && r->row_stride % 8 == 0 &&
+         r->head_stride % 8 == 0 && r->row_stride < (1ll << 40) && r->head_stride < (1ll << 40) && d > 0;
+}
+static Rows rows_of(const fa_rows* r) { return Rows{r->data, (long long)r->row_stride, (long long)r->head_stride}; }
+
+static fa_status check_cache(const fa_paged_cache* c, bool scales, PagedCache* p) {
+  if (!c || !c->K || !c->V || !c->page_table) return FA_ERR_INVALID_ARG;
+  if (c->dtype != FA_CACHE_BF16 && c->dtype != FA_CACHE_E4M3) return FA_ERR_INVALID_ARG;
+  if (c->num_pages <= 0 || c->page_size <= 0 || c->Hkv <= 0 || c->d <= 0 || c->B <= 0 || c->max_pages <= 0)
+    return FA_ERR_INVALID_ARG;
+  const int elem = c->dtype == FA_CACHE_E4M3 ? 1 : 2;
+  const int64_t unit = 16 / elem;  // every row starts on a 16-byte boundary
+  for (int64_t st : {c->page_stride, c->head_stride, c->row_stride})
+    if (st < 0 || st % unit != 0 || st >= (1ll << 40)) return FA_ERR_INVALID_ARG;
+  if (!aligned(c->K, 16) || !aligned(c->V, 16) || !aligned(c->page_table, 4) || c->table_stride < 0)
+    return FA_ERR_INVALID_ARG;
+  if (scales && elem == 1 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
+    return FA_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return FA_ERR_UNSUPPORTED;
+  // positions fit an int; rows of (sequence, head) and blocks of 128 keys too
+  const long long cap = (long long)c->max_pages * c->page_size;
+  if (cap > (1ll << 30) || (long long)c->B * c->Hkv > (1ll << 24) || c->B * (cap / 128 + 1) > (1ll << 30))
+    return FA_ERR_UNSUPPORTED;
+  *p = PagedCache{c->K, c->V, elem, c->num_pages, c->page_size, c->Hkv, c->d, (long long)c->page_stride,
+                  (long long)c->head_stride, (long long)c->row_stride, c->k_scale, c->v_scale, c->page_table, c->B,
+                  c->max_pages, (long long)c->table_stride};
+  return FA_OK;
+}
+
+fa_status fa_paged_append(const fa_paged_cache* cache, const fa_rows* K, const fa_rows* V, const int* cu_seqlens,
+                          const int* lens, int T, void* stream) {
+  PagedCache c;
+  const fa_status st = check_cache(cache, true, &c);
+  if (st != FA_OK) return st;
+  if (T < 0 || !cu_seqlens || !lens || !aligned(cu_seqlens, 4) || !aligned(lens, 4)) return FA_ERR_INVALID_ARG;
+  if (T > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if (T == 0) return FA_OK;
+  if (!valid_rows(K, c.d) || !valid_rows(V, c.d)) return FA_ERR_INVALID_ARG;
+  return launch_paged_append(c, rows_of(K), rows_of(V), cu_seqlens, lens, T, (cudaStream_t)stream);
+}
+
+size_t fa_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int64_t max_len, int weights) {
+  if (B <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128) || max_len <= 0) return 0;
+  if (max_len > (1ll << 30) || (long long)B * Hq > (1ll << 24)) return 0;
+  return paged_decode_workspace_bytes(B, Hq, d, max_len, weights != 0);
+}
+
+fa_status fa_paged_decode(const fa_paged_cache* cache, const fa_rows* Q, int Hq, const int* lens, float scale,
+                          float* weights, int64_t w_batch_stride, int64_t w_head_stride, int accumulate, void* O,
+                          float* LSE, void* workspace, size_t workspace_bytes, void* stream) {
+  PagedCache c;
+  const fa_status st = check_cache(cache, true, &c);
+  if (st != FA_OK) return st;
+  if (!valid_rows(Q, c.d) || Hq <= 0 || Hq % c.Hkv != 0 || !lens || !aligned(lens, 4)) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || !isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (!O || !LSE || !aligned(O, 16) || !aligned(LSE, 4)) return FA_ERR_INVALID_ARG;
+  if (weights && (!aligned(weights, 4) || w_batch_stride < 0 || w_head_stride < 0)) return FA_ERR_INVALID_ARG;
+  if ((long long)c.B * Hq > (1ll << 24)) return FA_ERR_UNSUPPORTED;
+  const size_t need = paged_decode_workspace_bytes(c.B, Hq, c.d, (long long)c.max_pages * c.page_size, weights != nullptr);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return FA_ERR_WORKSPACE;
+  PagedDecode a;
+  a.Q = rows_of(Q);
+  a.Hq = Hq;
+  a.lens = lens;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  a.W = weights;
+  a.w_batch = w_batch_stride;
+  a.w_head = w_head_stride;
+  a.accumulate = accumulate != 0;
+  a.O = O;
+  a.LSE = LSE;
+  a.workspace = workspace;
+  return launch_paged_decode(c, a, (cudaStream_t)stream);
+}
+
+fa_status fa_paged_evict(const fa_paged_cache* cache, const int* lens, const int* table_out, int64_t table_out_stride,
+                         int max_pages_out, const float* weights, int64_t w_batch_stride, int64_t w_head_stride,
+                         int budget, int recent, float* weights_out, int64_t wo_batch_stride, int64_t wo_head_stride,
+                         int64_t wo_len, int* kept, int* lens_out, void* stream) {
+  PagedCache c;
+  const fa_status st = check_cache(cache, false, &c);
+  if (st != FA_OK) return st;
+  if (!lens || !table_out || !weights || !weights_out || !kept || !lens_out) return FA_ERR_INVALID_ARG;
+  for (const void* q : {(const void*)lens, (const void*)table_out, (const void*)weights, (const void*)weights_out,
+                        (const void*)kept, (const void*)lens_out})
+    if (!aligned(q, 4)) return FA_ERR_INVALID_ARG;
+  if (table_out_stride < 0 || w_batch_stride < 0 || w_head_stride < 0 || wo_batch_stride < 0 || wo_head_stride < 0)
+    return FA_ERR_INVALID_ARG;
+  if (budget <= 0 || recent < 0 || recent > budget || max_pages_out <= 0) return FA_ERR_INVALID_ARG;
+  const long long cap = (long long)c.max_pages * c.page_size;
+  const long long most = cap < budget ? cap : budget;  // rows a sequence can be left with
+  if ((long long)max_pages_out * c.page_size < most || wo_len < most) return FA_ERR_INVALID_ARG;
+  if (wo_len > (1ll << 30) || budget > (1 << 30) || (long long)c.B * c.Hkv * (budget / 32 + 1) > (1ll << 30))
+    return FA_ERR_UNSUPPORTED;
+  Evict e{lens, table_out, (long long)table_out_stride, max_pages_out, weights, (long long)w_batch_stride,
+          (long long)w_head_stride, budget, recent, weights_out, (long long)wo_batch_stride,
+          (long long)wo_head_stride, (int)wo_len, kept, lens_out};
+  return launch_paged_evict(c, e, (cudaStream_t)stream);
+}
+
 fa_status fa_device_status(void* stream) {
   if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return FA_ERR_CUDA;
   uint32_t v = 0, zero = 0;

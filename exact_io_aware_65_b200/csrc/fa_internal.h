@@ -60,6 +60,58 @@ fa_status launch_decode(const Problem& p, const void* Q, const void* K, const vo
 size_t standard_workspace_bytes(int BH, int N);
 fa_status launch_standard_fwd(const Problem& p, const void* Q, const void* K, const void* V, void* O, float* LSE,
                               void* workspace, cudaStream_t s);
+// Rows of a packed tensor [rows, heads, d]; strides in elements.
+struct Rows {
+  void* data;
+  long long row_stride, head_stride;
+};
+
+// A paged cache after validation (strides in elements; elem: bytes of one).
+struct PagedCache {
+  void* K;
+  void* V;
+  int elem, num_pages, page_size, Hkv, d;
+  long long page_stride, head_stride, row_stride;
+  const float* k_scale;
+  const float* v_scale;
+  const int* table;
+  int B, max_pages;
+  long long table_stride;
+};
+
+struct PagedDecode {
+  Rows Q;
+  int Hq;
+  const int* lens;
+  float scale_log2;
+  float* W;  // accumulated weights, or nullptr
+  long long w_batch, w_head;
+  int accumulate;
+  void* O;
+  float* LSE;
+  void* workspace;
+};
+
+struct Evict {
+  const int* lens;
+  const int* table_out;
+  long long table_out_stride;
+  int max_out;
+  const float* W;
+  long long w_batch, w_head;
+  int budget, recent;
+  float* Wout;
+  long long wo_batch, wo_head;
+  int wo_len;
+  int* kept;
+  int* lens_out;
+};
+
+fa_status launch_paged_append(const PagedCache& c, const Rows& K, const Rows& V, const int* cu, const int* lens, int T,
+                              cudaStream_t s);
+size_t paged_decode_workspace_bytes(int B, int Hq, int d, long long cap, bool weights);
+fa_status launch_paged_decode(const PagedCache& c, const PagedDecode& a, cudaStream_t s);
+fa_status launch_paged_evict(const PagedCache& c, const Evict& e, cudaStream_t s);
 fa_status launch_selftest_wait(uint64_t timeout_ns, cudaStream_t s);
 fa_status launch_selftest_mma(const void* A, const void* B, float* C, int n, int k, int mode, cudaStream_t s);
 

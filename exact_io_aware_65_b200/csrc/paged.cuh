@@ -1,0 +1,159 @@
+// paged.cuh -- the paged key/value cache as the kernels see it: where the row
+// of a position lies, which packed token a row of the input is, and how the
+// decode call divides its work.  The functions are host-callable too, so that
+// a host test can walk them over any table, good or bad.
+#pragma once
+
+#include <stdint.h>
+
+#include "fa.h"
+#include "fa_internal.h"
+#include "sm100.cuh"
+
+namespace fa {
+namespace paged {
+
+// Device view of an fa_paged_cache.  Strides count bytes.
+struct Cache {
+  uint8_t* K;
+  uint8_t* V;
+  long long page_stride, head_stride, row_stride;
+  int num_pages, page_size;
+  const int* table;  // [B, max_pages], rows table_stride apart
+  int max_pages;
+  long long table_stride;
+  const float* k_scale;  // [Hkv], 8-bit pools only
+  const float* v_scale;
+};
+
+// Byte offset, in either pool, of head 0's row of a page's slot; -1 for a page
+// index outside the pool (the caller records FA_ERR_BOUNDS and skips the row).
+__host__ __device__ __forceinline__ long long row_offset(const Cache& c, int page, int slot) {
+  if (page < 0 || page >= c.num_pages) return -1;
+  return page * c.page_stride + slot * c.row_stride;
+}
+
+// The page index of position `pos` of sequence b; -1 past the table's width.
+__host__ __device__ __forceinline__ int page_of(const Cache& c, int b, long long pos) {
+  const long long i = pos / c.page_size;
+  if (pos < 0 || i >= c.max_pages) return -1;
+  return ld_ro(c.table + b * c.table_stride + i);
+}
+
+// Records a page index outside the pool.
+__device__ __forceinline__ void bad_page(uint32_t* status) { atomicCAS(status, FA_DEV_OK, FA_DEV_ERR_BOUNDS); }
+
+// A sequence's length as the kernels use it: at most what its table can hold.
+__host__ __device__ __forceinline__ int clamp_len(const Cache& c, int len) {
+  const long long cap = (long long)c.max_pages * c.page_size;
+  return len < 0 ? 0 : (int)(len < cap ? len : cap);
+}
+
+// ------------------------------------------------------------------ decode ---
+// The keys of each (sequence, head unit) form blocks of BLOCK keys, and the
+// blocks of all of them one row: sequence by sequence, unit by unit, in key
+// order.  CTA c of `grid` takes blocks [share(c), share(c + 1)), whatever
+// sequences these belong to, so that every CTA reads the same amount of cache
+// (to one block) however the lengths are spread.
+constexpr int WARPS = 8;
+constexpr int STEP = 16;             // keys a warp handles at a time
+constexpr int BLOCK = WARPS * STEP;  // keys of one block
+
+__host__ __device__ __forceinline__ int blocks_of(int len) { return (len + BLOCK - 1) / BLOCK; }
+__host__ __device__ __forceinline__ long long share(long long total, int grid, int c) { return total * c / grid; }
+
+// The CTA that holds block x: the largest c with share(c) <= x.
+__host__ __device__ __forceinline__ int owner(long long total, int grid, long long x) {
+  int c = (int)(x * grid / total);
+  while (c + 1 < grid && share(total, grid, c + 1) <= x) ++c;
+  while (c > 0 && share(total, grid, c) > x) --c;
+  return c;
+}
+
+// A CTA leaves at most two partial results: of the unit that began before its
+// first block (or with it), slot 2c, and of the one that goes on past its
+// last, slot 2c + 1; units between these are complete in it.
+__host__ __device__ __forceinline__ int part_slot(int c, long long cta_begin, long long unit_begin) {
+  return 2 * c + (cta_begin >= unit_begin ? 0 : 1);
+}
+
+// What the walk goes by.
+struct Work {
+  const Cache* c;
+  const int* lens;
+  int B, HU;  // sequences, head units of each
+};
+
+// A CTA's place in its blocks.
+struct Walk {
+  int b, hu, blk, nblk;  // sequence, head unit, block and blocks of the unit
+  int len;
+  long long at, end;     // place in the row of all blocks, and where the CTA stops
+};
+
+__host__ __device__ __forceinline__ void enter_sequence(const Work& k, Walk& w) {
+  w.len = clamp_len(*k.c, ld_ro(k.lens + w.b));
+  w.nblk = blocks_of(w.len);
+}
+
+// The start of CTA `cta` of `grid` <= total; prefix[b]: blocks of one head unit
+// in sequences 0 .. b.
+__host__ __device__ __forceinline__ Walk start_walk(const Work& k, const int* prefix, int b, long long total, int grid,
+                                                    int cta) {
+  Walk w;
+  w.at = cta < grid ? share(total, grid, cta) : total;
+  w.end = cta < grid ? share(total, grid, cta + 1) : total;
+  w.b = b;
+  w.hu = w.blk = w.nblk = w.len = 0;
+  if (w.at < w.end) {
+    enter_sequence(k, w);
+    const long long into = w.at - (b > 0 ? (long long)prefix[b - 1] * k.HU : 0);
+    w.hu = (int)(into / w.nblk);
+    w.blk = (int)(into % w.nblk);
+  }
+  return w;
+}
+
+// The sequence that holds block x: the first b with prefix[b] * HU > x.
+__host__ __device__ __forceinline__ int sequence_of(const int* prefix, int B, int HU, long long x) {
+  int lo = 0, hi = B;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if ((long long)prefix[mid] * HU > x) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// From the last block of a unit, `at` already past it, to the next unit.
+__host__ __device__ __forceinline__ void next_unit(const Work& k, Walk& w) {
+  w.blk = 0;
+  if (++w.hu < k.HU) return;
+  w.hu = 0;
+  if (w.at >= w.end) return;
+  do {  // at < end <= total: a sequence with blocks is ahead
+    ++w.b;
+    enter_sequence(k, w);
+  } while (w.nblk == 0 && w.b + 1 < k.B);
+}
+
+}  // namespace paged
+
+inline paged::Cache cache_view(const PagedCache& c) {
+  paged::Cache v;
+  v.K = static_cast<uint8_t*>(c.K);
+  v.V = static_cast<uint8_t*>(c.V);
+  v.page_stride = c.page_stride * c.elem;
+  v.head_stride = c.head_stride * c.elem;
+  v.row_stride = c.row_stride * c.elem;
+  v.num_pages = c.num_pages;
+  v.page_size = c.page_size;
+  v.table = c.table;
+  v.max_pages = c.max_pages;
+  v.table_stride = c.table_stride;
+  v.k_scale = c.k_scale;
+  v.v_scale = c.v_scale;
+  return v;
+}
+
+}  // namespace fa

@@ -64,8 +64,9 @@ typedef enum {
   FA_ERR_CUDA = 3,        /* a CUDA runtime or driver call failed */
   FA_ERR_WORKSPACE = 4,   /* workspace missing or smaller than fa_bwd_workspace_size() */
   FA_ERR_TIMEOUT = 5,     /* a bounded device-side wait ran out (see fa_device_status) */
-  FA_ERR_BOUNDS = 6       /* debug build only (libfa_debug.so): a kernel's index check
-                             found an access outside its buffer and skipped it */
+  FA_ERR_BOUNDS = 6       /* a kernel skipped an access outside its buffer: a page index outside the
+                             cache's pool (fa_paged_*), or, in the debug build (libfa_debug.so), any
+                             access that its index checks found out of range */
 } fa_status;
 
 typedef enum { FA_MASK_NONE = 0, FA_MASK_CAUSAL = 1, FA_MASK_BLOCK = 2 } fa_mask_kind;
@@ -200,6 +201,99 @@ fa_status fa_decode(const void* Q, const void* K, const void* V, int B, int H, i
                     int mask_kind, float scale, void* O, float* LSE, void* workspace,
                     size_t workspace_bytes, void* stream);
 
+/* ---- Paged key/value cache -------------------------------------------------
+ * A pool of pages shared by the sequences of a batch.  Position p of sequence
+ * b lies in slot p % page_size of page page_table[b][p / page_size]; the pools
+ * K and V hold, for each page, Hkv heads of page_size rows of d values.  Any
+ * page_size >= 1; the three strides (in elements, the same for both pools)
+ * give the order of pages, heads and rows, each a multiple of 16 bytes, with
+ * a row's d values contiguous.  dtype FA_CACHE_BF16, or FA_CACHE_E4M3: 8-bit
+ * floating point (4 exponent bits, 3 of fraction, largest 448, no infinity),
+ * an entry standing for its value times k_scale[h] (v_scale[h]) of its head.
+ * page_table: DEVICE int [B, max_pages], rows table_stride apart; entries are
+ * read only for positions that a sequence has.  A page index outside
+ * [0, num_pages) is not followed: its rows count as zeros (append and evict
+ * skip them) and the call records FA_ERR_BOUNDS in the device status word.
+ * Sequences may share pages that are only read. */
+typedef enum { FA_CACHE_BF16 = 0, FA_CACHE_E4M3 = 1 } fa_cache_dtype;
+
+typedef struct {
+  void* K; /* DEVICE pools, 16-byte aligned */
+  void* V;
+  int dtype;
+  int num_pages, page_size, Hkv, d;
+  int64_t page_stride, head_stride, row_stride;
+  const float* k_scale; /* DEVICE fp32 [Hkv], FA_CACHE_E4M3 only (append and decode) */
+  const float* v_scale;
+  const int* page_table;
+  int B, max_pages;
+  int64_t table_stride;
+} fa_paged_cache;
+
+/* Rows [rows, heads, d] of bf16 (one row a token), d contiguous, 16-byte
+ * aligned; strides in elements, multiples of 8: a slice of a fused projection
+ * needs no copy. */
+typedef struct {
+  void* data;
+  int64_t row_stride, head_stride;
+} fa_rows;
+
+/* Write new keys and values into the cache.
+ * In:  K, V: T rows of Hkv heads; row t belongs to the sequence b with
+ *      cu_seqlens[b] <= t < cu_seqlens[b+1] (DEVICE int [B+1], ascending) and
+ *      goes to position lens[b] + t - cu_seqlens[b] (lens: DEVICE int [B], the
+ *      positions already held; the call does not change it).  Rows that
+ *      belong to no sequence are not read.  T = 0 does nothing.
+ * Out: the pools' rows: a copy (FA_CACHE_BF16), or x / scale rounded to the
+ *      nearest 8-bit value, ties to even, magnitudes above 448 held at 448.
+ * Two rows that go to one slot (a page listed twice) leave either of them. */
+fa_status fa_paged_append(const fa_paged_cache* cache, const fa_rows* K, const fa_rows* V,
+                          const int* cu_seqlens, const int* lens, int T, void* stream);
+
+/* Attention of one new token per sequence over its cached keys, with grouped
+ * heads: query head h reads key head h / (Hq / Hkv), Hq a multiple of Hkv.  The
+ * cache already holds the token's own key (append first).
+ * In:  Q: B rows of Hq heads; lens (DEVICE int [B], clamped to [0, max_pages *
+ *      page_size]): every key below lens[b] is visible; scale > 0; workspace
+ *      (DEVICE, 256-byte aligned, fa_paged_decode_workspace_size() bytes with
+ *      max_len = max_pages * page_size; contents irrelevant on entry; calls
+ *      that may overlap need one each).
+ * Out: O [B, Hq, d] bf16, LSE [B, Hq] fp32 (natural log), contiguous; a
+ *      sequence without keys gets O = 0, LSE = -inf.  weights (may be NULL):
+ *      DEVICE fp32 [B, Hkv, max_pages * page_size] with the given strides in
+ *      elements; entry (b, k, j), j < lens[b], is set to (accumulate = 0), or
+ *      raised by, the attention that key j of key head k drew, summed over its
+ *      query heads; entries from lens[b] on are left as they are.
+ * The keys are divided evenly over the GPU whatever the lengths, and the parts
+ * joined in a fixed order: the same bits on every run. */
+size_t fa_paged_decode_workspace_size(int B, int Hq, int Hkv, int d, int64_t max_len, int weights);
+fa_status fa_paged_decode(const fa_paged_cache* cache, const fa_rows* Q, int Hq, const int* lens,
+                          float scale, float* weights, int64_t w_batch_stride, int64_t w_head_stride,
+                          int accumulate, void* O, float* LSE, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Shrink each sequence's cache to at most `budget` rows a head by the weights
+ * that fa_paged_decode accumulates.  Of a sequence with n > budget rows each
+ * key head keeps the last `recent` (0 <= recent <= budget) and, of those before
+ * them, the budget - recent of largest weight (equal weights: the lowest
+ * position; -0 equals 0; NaN is less than every number); a shorter sequence
+ * keeps all.  The kept rows are copied, in order, to positions 0, 1, ... of the
+ * pages of table_out (DEVICE int [B, max_pages_out] of the same pool, rows
+ * table_out_stride apart); the source rows stay as they are, so shared pages
+ * are no obstacle.  No page of table_out may be listed twice, or belong to the
+ * source of any sequence of the call: what such a page holds is undefined.
+ * In:  weights, fp32 as in fa_paged_decode; lens as there.
+ * Out: kept, DEVICE int [B, Hkv, budget]: the kept positions, ascending, then
+ *      -1; lens_out, DEVICE int [B]: min(lens[b], budget); weights_out, DEVICE
+ *      fp32 rows of wo_len >= min(budget, max_pages * page_size) entries: the
+ *      kept rows' weights, then zeros, ready for the next decode steps.
+ * Outputs must not alias inputs. */
+fa_status fa_paged_evict(const fa_paged_cache* cache, const int* lens, const int* table_out,
+                         int64_t table_out_stride, int max_pages_out, const float* weights,
+                         int64_t w_batch_stride, int64_t w_head_stride, int budget, int recent,
+                         float* weights_out, int64_t wo_batch_stride, int64_t wo_head_stride,
+                         int64_t wo_len, int* kept, int* lens_out, void* stream);
+
 /* Standard (materialising) attention, forward only: the baseline the pages
  * measure the method against, for speed and memory comparisons.  It writes
  * S = scale Q K^T to HBM in fp32, reads it back for a masked row softmax
@@ -256,8 +350,8 @@ fa_status fa_bwd_static_workspace(const void* Q, const void* K, const void* V, c
 
 /* Synchronise `stream`, then read and clear the calling device's status
  * word.  Returns FA_OK, FA_ERR_TIMEOUT if a bounded wait ran out in a kernel
- * since the last call, FA_ERR_BOUNDS if (debug build only) an index check
- * failed, or FA_ERR_CUDA if the synchronisation itself failed. */
+ * since the last call, FA_ERR_BOUNDS if a kernel skipped an access
+ * outside its buffer, or FA_ERR_CUDA if the synchronisation itself failed. */
 fa_status fa_device_status(void* stream);
 
 /* Set the wall-clock limit, in nanoseconds, of every device-side wait in
