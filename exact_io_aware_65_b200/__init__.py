@@ -49,6 +49,11 @@ SIGNATURES = {
                            _vp, _vp, _sz, _vp]),
     "fa_decode_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_decode": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _sz, _vp]),
+    "fa_fwd_packed_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "fa_fwd_packed": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _sz, _vp]),
+    "fa_bwd_packed_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "fa_bwd_packed": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _vp, _vp,
+                           _vp, _sz, _vp]),
     "fa_paged_append": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp]),
     "fa_paged_decode_workspace_size": (_sz, [_i, _i, _i, _i, _i64, _i]),
     "fa_paged_decode": (_i, [_vp, _vp, _i, _vp, _f, _vp, _i64, _i64, _i, _vp, _vp, _vp, _sz, _vp]),
@@ -374,12 +379,92 @@ def _int32(t, name, n, device):
     return t.data_ptr()
 
 
+def _sequences(cu):
+    """Number of sequences that an int32 vector of first rows [B + 1] describes."""
+    if not (isinstance(cu, torch.Tensor) and cu.dim() == 1 and cu.shape[0] >= 2):
+        raise FAError(1, "cu_q must be an int32 tensor [B + 1] with B >= 1")
+    return cu.shape[0] - 1
+
+
 def _table(t, name, device):
     """Pointer, width and row stride of a page table [B, pages] (int32)."""
     if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype == torch.int32 and t.dim() == 2
             and t.shape[0] > 0 and t.shape[1] > 0 and (t.stride(1) == 1 or t.shape[1] == 1)):
         raise FAError(1, f"{name} must be an int32 tensor [B, pages] on {device} with contiguous rows")
     return t.data_ptr(), t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _packed_mask(mask):
+    kind = MASKS[mask] if isinstance(mask, str) else int(mask)
+    if kind == MASKS["block"]:
+        raise FAError(2, "packed attention takes no block mask")
+    return kind
+
+
+def fwd_packed_workspace_size(B, Tq, Hq, Hkv, d) -> int:
+    return int(lib().fa_fwd_packed_workspace_size(B, Tq, Hq, Hkv, d))
+
+
+def fwd_packed(Q, K, V, cu_q, cu_k, mask="none", scale=None, O=None, LSE=None, workspace=None, stream=None):
+    """Attention over packed sequences with grouped heads: Q [Tq, Hq, d], K, V
+    [Tk, Hkv, d] bf16 (rows and heads may be strided), sequence b in rows
+    cu_q[b] .. cu_q[b + 1] of Q and cu_k[b] .. cu_k[b + 1] of K and V (int32
+    [B + 1]); mask "none" or "causal" (aligned at each sequence's last query and
+    key).  Returns O [Tq, Hq, d] bf16 and LSE [Hq, Tq] fp32; rows that belong to
+    no sequence are not written."""
+    q = _rows(Q, "Q")
+    dev = Q.device
+    Tq, Hq, d = Q.shape
+    k = _rows(K, "K", None, d, None, dev)
+    Tk, Hkv, _ = K.shape
+    v = _rows(V, "V", Hkv, d, Tk, dev)
+    B = _sequences(cu_q)
+    scale = d ** -0.5 if scale is None else float(scale)
+    if O is None:
+        O = _empty((Tq, Hq, d), torch.bfloat16, dev, stream)
+    o = _rows(O, "O", Hq, d, Tq, dev)
+    LSE = _empty((Hq, Tq), torch.float32, dev, stream) if LSE is None else \
+        _check_buf(LSE, "LSE", (Hq, Tq), torch.float32, dev)
+    need = fwd_packed_workspace_size(B, Tq, Hq, Hkv, d)
+    if workspace is None and need:
+        workspace = _empty(need, torch.uint8, dev, stream)
+    wp, wn = (None, 0) if workspace is None else _workspace(workspace, need, dev)
+    _run("fa_fwd_packed", dev, stream, ctypes.byref(q), ctypes.byref(k), ctypes.byref(v),
+         _int32(cu_q, "cu_q", B + 1, dev), _int32(cu_k, "cu_k", B + 1, dev), B, Tq, Tk, Hq, Hkv, d, _packed_mask(mask),
+         scale, ctypes.byref(o), LSE.data_ptr(), wp, wn)
+    return O, LSE
+
+
+def bwd_packed_workspace_size(B, Tq, Tk, Hq, Hkv, d) -> int:
+    return int(lib().fa_bwd_packed_workspace_size(B, Tq, Tk, Hq, Hkv, d))
+
+
+def bwd_packed(Q, K, V, O, dO, LSE, cu_q, cu_k, mask="none", scale=None, dQ=None, dK=None, dV=None, workspace=None,
+               stream=None, deterministic=False):
+    """The gradients of ``fwd_packed``: dQ [Tq, Hq, d], dK, dV [Tk, Hkv, d]
+    (summed over each key head's query heads) from O and LSE of the forward
+    with the same mask and scale."""
+    q = _rows(Q, "Q")
+    dev = Q.device
+    Tq, Hq, d = Q.shape
+    k = _rows(K, "K", None, d, None, dev)
+    Tk, Hkv, _ = K.shape
+    v = _rows(V, "V", Hkv, d, Tk, dev)
+    o, g = _rows(O, "O", Hq, d, Tq, dev), _rows(dO, "dO", Hq, d, Tq, dev)
+    _check_buf(LSE, "LSE", (Hq, Tq), torch.float32, dev)
+    B = _sequences(cu_q)
+    scale = d ** -0.5 if scale is None else float(scale)
+    dQ, dK, dV = (_empty((T, H, d), torch.bfloat16, dev, stream) if t is None else t
+                  for t, T, H in ((dQ, Tq, Hq), (dK, Tk, Hkv), (dV, Tk, Hkv)))
+    dq, dk, dv = _rows(dQ, "dQ", Hq, d, Tq, dev), _rows(dK, "dK", Hkv, d, Tk, dev), _rows(dV, "dV", Hkv, d, Tk, dev)
+    need = bwd_packed_workspace_size(B, Tq, Tk, Hq, Hkv, d)
+    if workspace is None:
+        workspace = _empty(need, torch.uint8, dev, stream)
+    wp, wn = _workspace(workspace, need, dev)
+    _run("fa_bwd_packed", dev, stream, ctypes.byref(q), ctypes.byref(k), ctypes.byref(v), ctypes.byref(o), ctypes.byref(g),
+         LSE.data_ptr(), _int32(cu_q, "cu_q", B + 1, dev), _int32(cu_k, "cu_k", B + 1, dev), B, Tq, Tk, Hq, Hkv, d,
+         _packed_mask(mask), scale, 1 if deterministic else 0, ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), wp, wn)
+    return dQ, dK, dV
 
 
 def _paged_cache(k_cache, v_cache, page_table, k_scale=None, v_scale=None, scales=True):

@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "fa.h"
+#include "pack.cuh"
 #include "sm100.cuh"
 
 namespace fa {
@@ -38,6 +39,12 @@ struct Params {
   __nv_bfloat16* dV;
   uint64_t timeout_ns;
   uint32_t* status;
+  // PACKED: the sequences; parts that a key head's query heads are divided
+  // into (each part is an item of its own), and where dK and dV of a part go.
+  Pack pk;
+  int d, parts;
+  float* part;  // [parts][2 (dV, dK)][Tk][Hkv][d], or nullptr: one part, straight to dK and dV
+  long long dk_row, dk_head, dv_row, dv_head;  // strides of dK and dV, elements
 };
 
 // Heads per scheduling group.  The group's Q and dO tiles (bf16) and fp32
@@ -54,6 +61,9 @@ __host__ __device__ inline int sched_group(int BH, int N, int d) {
 struct Item {
   int bh, j;
   int Lq, Lk, off, nqb;  // this sequence's query rows and keys, causal offset, query tiles
+  // PACKED: key head, query heads [g0, g1) of it, part, first query row and key,
+  // first slot of the query tiles; off counts tiles.
+  int hk, g0, g1, part, sq, sk, slot;
 };
 
 // Work item idx -> (head, key tile).  Heads are taken in groups of
@@ -61,7 +71,7 @@ struct Item {
 // to a few heads and stay in L2; within a group low key tiles come first
 // (under a causal mask they meet the most query tiles and run longest).
 
-template <bool VARLEN>
+template <int MODE>
 __host__ __device__ __forceinline__ Item item_at(const Params& p, int idx) {
   const int per_group = p.group * p.nk;
   const int g = idx / per_group, r = idx % per_group;
@@ -69,7 +79,7 @@ __host__ __device__ __forceinline__ Item item_at(const Params& p, int idx) {
   Item it;
   it.j = r / gsize;
   it.bh = g * p.group + r % gsize;
-  if (VARLEN) {
+  if (MODE == PADDED) {
     const int b = it.bh / p.H;
     const bool bok = FA_IN_BOUNDS(p.status, b, 1, p.BH / p.H);
     it.Lq = p.seqlens_q ? (bok ? min(max(ld_ro(p.seqlens_q + b), 0), p.N) : 0) : p.N;
@@ -105,10 +115,10 @@ __host__ __device__ __forceinline__ uint32_t add_rank(const Params& p, int j, in
 // Next query tile >= i of the sequence that attends to key tile j (p.nq if
 // none; a key tile past the sequence's keys has none).  Causal: the rows
 // that see some key of tile j are those >= j * BK - off.
-template <bool VARLEN>
+template <int MODE>
 __host__ __device__ __forceinline__ int next_q(const Params& p, const Item& it, int i) {
   const int j = it.j;
-  if (VARLEN && j * BK >= it.Lk) return p.nq;
+  if (MODE == PADDED && j * BK >= it.Lk) return p.nq;
   if (p.mask_kind == FA_MASK_CAUSAL) {
     const int first = max(0, j * BK - it.off) / BQ;
     if (i < first) i = first;
@@ -118,7 +128,65 @@ __host__ __device__ __forceinline__ int next_q(const Params& p, const Item& it, 
           ld_ro(p.block_mask + (size_t)i * p.nk + j))
         break;
   }
-  return (!VARLEN || i < it.nqb) ? i : p.nq;
+  return (MODE != PADDED || i < it.nqb) ? i : p.nq;
+}
+
+// An item's steps: its query tiles, and for packed sequences those of each of
+// its query heads in turn.
+struct Step {
+  int i, g;
+};
+template <int MODE>
+__host__ __device__ __forceinline__ int packed_first(const Params& p, const Item& it) {
+  return p.mask_kind == FA_MASK_CAUSAL ? max(0, it.j - it.off) : 0;
+}
+template <int MODE>
+__host__ __device__ __forceinline__ Step first_step(const Params& p, const Item& it) {
+  if (MODE == PACKED) {
+    const int i = packed_first<MODE>(p, it);
+    return Step{i, i < it.nqb ? it.g0 : it.g1};
+  }
+  return Step{next_q<MODE>(p, it, 0), 0};
+}
+template <int MODE>
+__host__ __device__ __forceinline__ bool more(const Params& p, const Item& it, const Step& s) {
+  return MODE == PACKED ? s.g < it.g1 : s.i < p.nq;
+}
+template <int MODE>
+__host__ __device__ __forceinline__ Step next_step(const Params& p, const Item& it, const Step& s) {
+  if (MODE == PACKED) return s.i + 1 < it.nqb ? Step{s.i + 1, s.g} : Step{packed_first<MODE>(p, it), s.g + 1};
+  return Step{next_q<MODE>(p, it, s.i + 1), 0};
+}
+
+// Packed sequences: a sequence's items are its key tiles (the first see the
+// most query tiles under a causal mask) times the parts of its key heads.
+__host__ __device__ __forceinline__ pack::Units packed_units(const Params& p, const pack::Seq& s) {
+  pack::Units u;
+  u.tiles = pack::tiles(s.Lk);
+  u.heads = p.pk.Hkv * p.parts;
+  // whole key heads, the Q, dO and dQ of their query heads kept to about 64 MiB (as sched_group)
+  const long long fit = (64LL << 20) / (8LL * max(s.Lq, 1) * p.d * p.pk.G);
+  const long long least = (8 + p.pk.G - 1) / p.pk.G;  // 8 query heads
+  u.group = (int)min((long long)p.pk.Hkv, max(fit, least)) * p.parts;
+  return u;
+}
+
+__host__ __device__ __forceinline__ Item packed_item(const Params& p, const pack::Seq& s, int b, const pack::Place& at) {
+  Item it;
+  it.bh = 0;
+  it.j = at.tile;
+  it.Lq = s.Lq;
+  it.Lk = s.Lk;
+  it.nqb = pack::tiles(s.Lq);
+  it.off = pack::tiles(s.Lk) - it.nqb;
+  it.sq = s.sq;
+  it.sk = s.sk;
+  it.slot = pack::slot_base(s.sq, b);
+  it.hk = at.head / p.parts;
+  it.part = at.head % p.parts;
+  it.g0 = it.part * p.pk.G / p.parts;
+  it.g1 = (it.part + 1) * p.pk.G / p.parts;
+  return it;
 }
 
 }  // namespace bwd

@@ -83,6 +83,31 @@ bool make_map_bf16_box(CUtensorMap* map, const void* base, int BH, int N, int d,
   return r == CUDA_SUCCESS;
 }
 
+bool make_map_rows(CUtensorMap* map, const Rows& t, int T, int heads, int d, int box_cols, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn || (box_cols != 32 && box_cols != 64)) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)t.row_stride * 2, (cuuint64_t)t.head_stride * 2};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapSwizzle sw = box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            sw, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_map_packed(CUtensorMap* map, const Rows& t, int T, int heads, int d) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)T, (cuuint64_t)heads};
+  const cuuint64_t row = (cuuint64_t)t.row_stride * 2;
+  cuuint64_t strides[3] = {row, row, (cuuint64_t)t.head_stride * 2};
+  cuuint32_t box[4] = {64, 128, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t.data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_map_bf16_2d(CUtensorMap* map, const void* base, int rows, int cols, int box_rows) {
   return make_map_bf16(map, base, 1, rows, cols, box_rows);
 }
@@ -276,13 +301,94 @@ fa_status fa_standard_fwd(const void* Q, const void* K, const void* V, int B, in
   return launch_standard_fwd(p, Q, K, V, O, LSE, workspace, (cudaStream_t)stream);
 }
 
-// ---- paged cache ----
+// ---- packed sequences ----
 static bool valid_rows(const fa_rows* r, int d) {
   return r && r->data && aligned(r->data, 16) && r->row_stride >= 0 && r->head_stride >= 0 && r->row_stride % 8 == 0 &&
          r->head_stride % 8 == 0 && r->row_stride < (1ll << 40) && r->head_stride < (1ll << 40) && d > 0;
 }
 static Rows rows_of(const fa_rows* r) { return Rows{r->data, (long long)r->row_stride, (long long)r->head_stride}; }
 
+// Rows that the tensor maps take: strides above zero (of one row or head: never used).
+static bool valid_packed(const fa_rows* r, int T, int heads, int d, Rows* out) {
+  if (T == 0) {  // nothing to read: no data, any strides
+    *out = Rows{nullptr, d, d};
+    return true;
+  }
+  if (!valid_rows(r, d) || (T > 1 && r->row_stride == 0) || (heads > 1 && r->head_stride == 0)) return false;
+  *out = rows_of(r);
+  if (out->row_stride == 0) out->row_stride = d;
+  if (out->head_stride == 0) out->head_stride = d;
+  return true;
+}
+
+static bool packed_sizes_supported(int B, int Tq, int Tk, int Hq, int Hkv) {
+  // tiles x heads, and rows x heads of LSE, in 32 bits
+  return Tq <= (1 << 28) && Tk <= (1 << 28) && B <= (1 << 24) && Hkv <= Hq &&
+         (pack::slots(Tq, B) + 1) * Hq <= (1ll << 29) && (pack::slots(Tk, B) + 1) * Hq <= (1ll << 29);
+}
+
+static fa_status check_packed(const int* cu_q, const int* cu_k, int B, int Tq, int Tk, int Hq, int Hkv, int d,
+                              int mask_kind, float scale, PackedProblem* p) {
+  if (B <= 0 || Tq < 0 || Tk < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || d <= 0) return FA_ERR_INVALID_ARG;
+  if (!cu_q || !cu_k || !aligned(cu_q, 4) || !aligned(cu_k, 4)) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || !isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (mask_kind == FA_MASK_BLOCK) return FA_ERR_UNSUPPORTED;
+  if (mask_kind != FA_MASK_NONE && mask_kind != FA_MASK_CAUSAL) return FA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || !packed_sizes_supported(B, Tq, Tk, Hq, Hkv)) return FA_ERR_UNSUPPORTED;
+  p->pk = Pack{cu_q, cu_k, B, Tq, Tk, Hq, Hkv, Hq / Hkv};
+  p->d = d;
+  p->mask_kind = mask_kind;
+  p->scale = scale;
+  p->scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  return FA_OK;
+}
+
+fa_status fa_fwd_packed(const fa_rows* Q, const fa_rows* K, const fa_rows* V, const int* cu_q, const int* cu_k, int B,
+                        int Tq, int Tk, int Hq, int Hkv, int d, int mask_kind, float scale, const fa_rows* O,
+                        float* LSE, void* workspace, size_t workspace_bytes, void* stream) {
+  PackedProblem p;
+  const fa_status st = check_packed(cu_q, cu_k, B, Tq, Tk, Hq, Hkv, d, mask_kind, scale, &p);
+  if (st != FA_OK) return st;
+  Rows q, k, v, o;
+  if (!valid_packed(Q, Tq, Hq, d, &q) || !valid_packed(K, Tk, Hkv, d, &k) || !valid_packed(V, Tk, Hkv, d, &v) ||
+      !valid_packed(O, Tq, Hq, d, &o))
+    return FA_ERR_INVALID_ARG;
+  if (Tq == 0) return FA_OK;
+  if (!LSE || !aligned(LSE, 4)) return FA_ERR_INVALID_ARG;
+  return launch_fwd_packed(p, q, k, v, o, LSE, (cudaStream_t)stream);
+}
+
+size_t fa_fwd_packed_workspace_size(int B, int Tq, int Hq, int Hkv, int d) {
+  return 0;
+}
+
+size_t fa_bwd_packed_workspace_size(int B, int Tq, int Tk, int Hq, int Hkv, int d) {
+  if (B <= 0 || Tq < 0 || Tk < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  if (!packed_sizes_supported(B, Tq, Tk, Hq, Hkv)) return 0;
+  return bwd_packed_workspace_bytes(Pack{nullptr, nullptr, B, Tq, Tk, Hq, Hkv, Hq / Hkv}, d);
+}
+
+fa_status fa_bwd_packed(const fa_rows* Q, const fa_rows* K, const fa_rows* V, const fa_rows* O, const fa_rows* dO,
+                        const float* LSE, const int* cu_q, const int* cu_k, int B, int Tq, int Tk, int Hq, int Hkv,
+                        int d, int mask_kind, float scale, int deterministic, const fa_rows* dQ, const fa_rows* dK,
+                        const fa_rows* dV, void* workspace, size_t workspace_bytes, void* stream) {
+  PackedProblem p;
+  const fa_status st = check_packed(cu_q, cu_k, B, Tq, Tk, Hq, Hkv, d, mask_kind, scale, &p);
+  if (st != FA_OK) return st;
+  p.deterministic = deterministic ? 1 : 0;
+  Rows q, k, v, o, g, dq, dk, dv;
+  if (!valid_packed(Q, Tq, Hq, d, &q) || !valid_packed(K, Tk, Hkv, d, &k) || !valid_packed(V, Tk, Hkv, d, &v) ||
+      !valid_packed(O, Tq, Hq, d, &o) || !valid_packed(dO, Tq, Hq, d, &g) || !valid_packed(dQ, Tq, Hq, d, &dq) ||
+      !valid_packed(dK, Tk, Hkv, d, &dk) || !valid_packed(dV, Tk, Hkv, d, &dv))
+    return FA_ERR_INVALID_ARG;
+  if (Tq > 0 && (!LSE || !aligned(LSE, 4))) return FA_ERR_INVALID_ARG;
+  if (Tq == 0 && Tk == 0) return FA_OK;
+  const size_t need = bwd_packed_workspace_bytes(p.pk, d);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return FA_ERR_WORKSPACE;
+  return launch_bwd_packed(p, q, k, v, o, g, LSE, dq, dk, dv, workspace, (cudaStream_t)stream);
+}
+
+// ---- paged cache ----
 static fa_status check_cache(const fa_paged_cache* c, bool scales, PagedCache* p) {
   if (!c || !c->K || !c->V || !c->page_table) return FA_ERR_INVALID_ARG;
   if (c->dtype != FA_CACHE_BF16 && c->dtype != FA_CACHE_E4M3) return FA_ERR_INVALID_ARG;

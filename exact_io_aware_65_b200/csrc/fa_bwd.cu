@@ -176,6 +176,128 @@ __global__ void __launch_bounds__(256) dq_convert_kernel(const float* __restrict
   }
 }
 
+// ------------------------------------------------------- packed sequences ---
+struct PackedArgs {
+  Pack pk;
+  const __nv_bfloat16* O;
+  const __nv_bfloat16* dO;
+  long long o_row, o_head, do_row, do_head;  // elements
+  const float* LSE;                          // [Hq, Tq]
+  float* Dw;
+  float* L2w;
+  float* dq_acc;
+  uint32_t* sched;
+  uint32_t* turn;
+  __nv_bfloat16* dQ;
+  __nv_bfloat16* dK;
+  __nv_bfloat16* dV;
+  long long dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
+  const float* part;  // [parts][2][Tk][Hkv][d] or nullptr
+  int parts;
+  float scale;
+  uint32_t* status;
+};
+
+// The workspace rows of slot x (a query tile) and head h: (x Hq + h) 128 ...
+// A block per (slot, head), as prep_kernel.
+template <int D>
+__global__ void __launch_bounds__(256) packed_prep_kernel(const PackedArgs a) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, li = lane % LPR;
+  const int slot = blockIdx.x / a.pk.Hq, h = blockIdx.x % a.pk.Hq;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.sched = 0u;
+  const int b = pack::sequence_of_slot(a.pk, slot);
+  if (b < 0) return;
+  const pack::Seq s = pack::seq_at(a.pk, b);
+  const int i = slot - pack::slot_base(s.sq, b);
+  if (i >= pack::tiles(s.Lq)) return;  // a slot that no tile uses
+  if (threadIdx.x == 0) a.turn[blockIdx.x] = 0u;
+  const int first = i * 128 - pack::pad(s.Lq);  // row of the sequence (negative: none)
+  for (int r = (threadIdx.x >> 5) * RPW + sub; r < 128; r += 8 * RPW) {
+    const int n = first + r;
+    float acc = 0.0f;
+    if (n >= 0 && FA_IN_BOUNDS(a.status, s.sq + n, 1, a.pk.Tq)) {
+      const long long t = s.sq + n;
+      const uint4 x = *reinterpret_cast<const uint4*>(a.O + t * a.o_row + h * a.o_head + li * 8);
+      const uint4 y = *reinterpret_cast<const uint4*>(a.dO + t * a.do_row + h * a.do_head + li * 8);
+      const uint32_t av[4] = {x.x, x.y, x.z, x.w}, bv[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 fa2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&av[e]));
+        const float2 fb2 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&bv[e]));
+        acc = fmaf(fa2.x, fb2.x, acc);
+        acc = fmaf(fa2.y, fb2.y, acc);
+      }
+    }
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+    const size_t row = (size_t)blockIdx.x * 128 + r;
+    if (li == 0) {
+      a.Dw[row] = -acc;
+      float l2 = INFINITY;  // rows before the sequence, and rows that saw no key: P = 0
+      if (n >= 0) {
+        const float lse = a.LSE[(size_t)h * a.pk.Tq + s.sq + n];
+        if (lse > -INFINITY) l2 = lse * LOG2E;
+      }
+      a.L2w[row] = -l2;
+    }
+    float4* z = reinterpret_cast<float4*>(a.dq_acc + row * D + li * 8);
+    z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+    z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+
+// dQ = bf16(scale * accumulator), a block per (slot, head); the blocks behind
+// these add up the parts of dK and dV, in order.
+template <int D>
+__global__ void __launch_bounds__(256) packed_convert_kernel(const PackedArgs a, unsigned dq_blocks) {
+  constexpr int G = 4;  // four 4-column groups a thread, as dq_convert_kernel
+  if (blockIdx.x < dq_blocks) {
+    const int slot = blockIdx.x / a.pk.Hq, h = blockIdx.x % a.pk.Hq;
+    const int b = pack::sequence_of_slot(a.pk, slot);
+    if (b < 0) return;
+    const pack::Seq s = pack::seq_at(a.pk, b);
+    const int i = slot - pack::slot_base(s.sq, b);
+    if (i >= pack::tiles(s.Lq)) return;
+    const int first = i * 128 - pack::pad(s.Lq);
+    const float4* t = reinterpret_cast<const float4*>(a.dq_acc + (size_t)blockIdx.x * 128 * D);
+#pragma unroll
+    for (int k = threadIdx.x; k < 128 * (D / (4 * G)); k += 256) {
+      const int eb = k / 128, r = k % 128, n = first + r;
+      if (n < 0 || !FA_IN_BOUNDS(a.status, s.sq + n, 1, a.pk.Tq)) continue;
+      uint4* dst = reinterpret_cast<uint4*>(a.dQ + (long long)(s.sq + n) * a.dq_row + h * a.dq_head + 4 * G * eb);
+#pragma unroll
+      for (int u = 0; u < G / 2; ++u) {
+        const float4 x = t[(eb * G + 2 * u) * 128 + r], y = t[(eb * G + 2 * u + 1) * 128 + r];
+        dst[u] = make_uint4(pack_bf16x2(x.x * a.scale, x.y * a.scale), pack_bf16x2(x.z * a.scale, x.w * a.scale),
+                            pack_bf16x2(y.x * a.scale, y.y * a.scale), pack_bf16x2(y.z * a.scale, y.w * a.scale));
+      }
+    }
+    return;
+  }
+  // eight columns a thread; rows that belong to no sequence have no parts
+  const long long per = (long long)a.pk.Tk * a.pk.Hkv * (D / 8);
+  const int k0 = max(__ldg(a.pk.cu_k), 0), k1 = __ldg(a.pk.cu_k + a.pk.B);
+  for (long long k = (long long)(blockIdx.x - dq_blocks) * 256 + threadIdx.x; k < 2 * per;
+       k += (long long)(gridDim.x - dq_blocks) * 256) {
+    const int g = k >= per;  // 0: dV, 1: dK
+    const long long e = g ? k - per : k;
+    const long long row = e / (a.pk.Hkv * (D / 8));
+    const int hk = (int)(e / (D / 8) % a.pk.Hkv), c = (int)(e % (D / 8));
+    if (row < k0 || row >= k1) continue;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    for (int u = 0; u < a.parts; ++u) {
+      const float4* src = reinterpret_cast<const float4*>(a.part) + (((long long)u * 2 + g) * per + e) * 2;
+      const float4 p0 = src[0], p1 = src[1];
+      x = make_float4(x.x + p0.x, x.y + p0.y, x.z + p0.z, x.w + p0.w);
+      y = make_float4(y.x + p1.x, y.y + p1.y, y.z + p1.z, y.w + p1.w);
+    }
+    __nv_bfloat16* dst = g ? a.dK + row * a.dk_row + hk * a.dk_head : a.dV + row * a.dv_row + hk * a.dv_head;
+    *reinterpret_cast<uint4*>(dst + 8 * c) =
+        make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+  }
+}
+
 // ------------------------------------------------------------------ main ---
 template <int D>
 struct Cfg {
@@ -277,8 +399,12 @@ __device__ bool wait_turn(const uint32_t* a, uint32_t want, const WaitCtx& w) {
 constexpr int RING = 4;     // depth of the item ring the producer fills
 constexpr int CONSUMERS = 13;  // MMA warp + 8 softmax warps + 4 drain warps
 
-// VARLEN: per-sequence lengths are read (else every sequence has N, Nk).
-template <int D, bool VARLEN>
+// MODE: FIXED, every sequence has N, Nk; PADDED, per-sequence lengths are read;
+// PACKED, packed rows and grouped heads (the maps of Q, K, V and dO then have a
+// fourth dimension, the head, behind the sequence's first row).  A PACKED item
+// adds the gradients of all query heads of its part of a key head in tensor
+// memory, so grouped heads need no additions through memory either.
+template <int D, int MODE>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     main_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                 const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapdO,
@@ -309,6 +435,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // and passes them to the other roles through this ring.
   __shared__ __align__(8) uint64_t item_full[RING], item_empty[RING];
   __shared__ int item_ring[RING];
+  __shared__ int4 item_desc[MODE == PACKED ? RING : 1][2];  // PACKED: what the producer found the item to be
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
 
@@ -366,77 +493,143 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* sQD = smem + C::OFF_QD;
   const float* sLD = reinterpret_cast<const float*>(smem + C::OFF_LD);
 
-  // Consumer side of the item ring: the k-th item this CTA processes.
-  auto take_item = [&](uint32_t k, int& idx) -> bool {
+  // Consumer side of the item ring: the k-th item this CTA processes
+  // (idx >= n_items: no more).
+  auto read_item = [&](uint32_t slot, int& idx, Item& it) {
+    idx = *reinterpret_cast<volatile int*>(&item_ring[slot]);
+    if (MODE == PACKED) {
+      const int4 a = item_desc[slot][0], b = item_desc[slot][1];
+      it.j = a.x;
+      it.hk = a.y;
+      it.part = a.z;
+      it.slot = a.w;
+      it.g0 = it.part * p.pk.G / p.parts;
+      it.g1 = (it.part + 1) * p.pk.G / p.parts;
+      it.sq = b.x;
+      it.Lq = b.y;
+      it.sk = b.z;
+      it.Lk = b.w;
+      it.nqb = pack::tiles(it.Lq);
+      it.off = pack::tiles(it.Lk) - it.nqb;
+    }
+  };
+  auto take_item = [&](uint32_t k, int& idx, Item& it) -> bool {
     const uint32_t slot = k % RING;
     if (!mbar_wait(&item_full[slot], (k / RING) & 1, w)) return false;
-    idx = *reinterpret_cast<volatile int*>(&item_ring[slot]);
+    read_item(slot, idx, it);
     mbar_arrive(&item_empty[slot]);
+    if (MODE != PACKED && idx < p.n_items) it = item_at<MODE>(p, idx);
     return true;
   };
-  auto take_item_warp = [&](uint32_t k, int& idx) -> bool {
+  auto take_item_warp = [&](uint32_t k, int& idx, Item& it) -> bool {
     const uint32_t slot = k % RING;
     if (!mbar_wait_warp(&item_full[slot], (k / RING) & 1, w)) return false;
-    idx = *reinterpret_cast<volatile int*>(&item_ring[slot]);
+    read_item(slot, idx, it);
     __syncwarp();
     if (lane == 0) mbar_arrive(&item_empty[slot]);
+    if (MODE != PACKED && idx < p.n_items) it = item_at<MODE>(p, idx);
     return true;
   };
+  // First row of a step's query tile in the workspace's padded rows, and their number.
+  auto row_of = [&](const Item& it, const Step& q) -> size_t {
+    if (MODE == PACKED) return ((size_t)(it.slot + q.i) * p.pk.Hq + it.hk * p.pk.G + q.g) * BQ;
+    return (size_t)it.bh * p.Npad + (size_t)q.i * BQ;
+  };
+  [[maybe_unused]] const size_t ws_rows = (size_t)p.BH * p.Npad;  // PACKED: BH heads, Npad rows of all slots
 
   if (warp < 4) {
     regs_dec<C::REG_CTL>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    // One thread; PACKED: the warp looks the items up together, and lane 0
+    // issues the copies.
+    if (MODE == PACKED || lane == 0) {
+      const bool lead = MODE != PACKED || lane == 0;
+      auto await = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return MODE == PACKED ? mbar_wait_warp(bar, parity, w) : mbar_wait(bar, parity, w);
+      };
+      auto load = [&](uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int c, int y, int start, int head) {
+        if (MODE == PACKED) tma_load_4d(dst + c * C::CHUNK_BYTES, m, bar, c * 64, y, start, head);
+        else tma_load_3d(dst + c * C::CHUNK_BYTES, m, bar, c * 64, y, head);
+      };
+      pack::Walker walk;
       uint32_t item_iter = 0, qd_iter = 0;
       bool ok = true, q_only = false;  // q_only: the last tile's dO load was never issued
       for (;; ++item_iter) {
         const uint32_t slot = item_iter % RING;
-        ok = mbar_wait(&item_empty[slot], ((item_iter / RING) & 1) ^ 1, w);
+        ok = await(&item_empty[slot], ((item_iter / RING) & 1) ^ 1);
         if (!ok) break;
         // CTA b starts on item b, then claims items gridDim.x, gridDim.x + 1, ...
-        int idx = item_iter == 0 ? (int)blockIdx.x : (int)gridDim.x + (int)atomicAdd(p.sched, 1u);
-        if (idx > p.n_items) idx = p.n_items;
-        item_ring[slot] = idx;
-        mbar_arrive(&item_full[slot]);
-        if (idx >= p.n_items) break;
-        const Item it = item_at<VARLEN>(p, idx);
-        ok = mbar_wait(&kv_empty, (item_iter & 1) ^ 1, w);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&kv_full, 2 * C::TILE_BYTES);
-#pragma unroll
-        for (int c = 0; c < C::CHUNKS; ++c) {
-          tma_load_3d(sK + c * C::CHUNK_BYTES, &mapK, &kv_full, c * 64, it.j * BK, it.bh);
-          tma_load_3d(sV + c * C::CHUNK_BYTES, &mapV, &kv_full, c * 64, it.j * BK, it.bh);
+        int idx = (int)blockIdx.x;
+        if (item_iter > 0) {
+          if (lead) idx = (int)gridDim.x + (int)atomicAdd(p.sched, 1u);
+          if (MODE == PACKED) idx = __shfl_sync(0xffffffffu, idx, 0);
         }
-        for (int i = next_q<VARLEN>(p, it, 0); i < p.nq; i = next_q<VARLEN>(p, it, i + 1)) {
+        if (idx > p.n_items) idx = p.n_items;
+        Item it;
+        if (MODE == PACKED) {
+          int b;
+          pack::Seq sq;
+          pack::Place at;
+          if (idx < p.n_items && pack::locate(p.pk, walk, idx, [&](const pack::Seq& x) { return packed_units(p, x); },
+                                              [](const pack::Seq& x) { return x.Lq; }, b, sq, at))
+            it = packed_item(p, sq, b, at);
+          else
+            idx = p.n_items;
+        } else if (idx < p.n_items) {
+          it = item_at<MODE>(p, idx);
+        }
+        if (lead) {
+          item_ring[slot] = idx;
+          if (MODE == PACKED && idx < p.n_items) {
+            item_desc[slot][0] = make_int4(it.j, it.hk, it.part, it.slot);
+            item_desc[slot][1] = make_int4(it.sq, it.Lq, it.sk, it.Lk);
+          }
+          mbar_arrive(&item_full[slot]);
+        }
+        if (idx >= p.n_items) break;
+        ok = await(&kv_empty, (item_iter & 1) ^ 1);
+        if (!ok) break;
+        const int yq = MODE == PACKED ? -pack::pad(it.Lq) : 0, yk = MODE == PACKED ? -pack::pad(it.Lk) : 0;
+        if (lead) {
+          mbar_arrive_expect_tx(&kv_full, 2 * C::TILE_BYTES);
+          const int head = MODE == PACKED ? it.hk : it.bh;
+#pragma unroll
+          for (int c = 0; c < C::CHUNKS; ++c) {
+            load(sK, &mapK, &kv_full, c, yk + it.j * BK, it.sk, head);
+            load(sV, &mapV, &kv_full, c, yk + it.j * BK, it.sk, head);
+          }
+        }
+        for (Step i = first_step<MODE>(p, it); more<MODE>(p, it, i); i = next_step<MODE>(p, it, i)) {
           const uint32_t st = qd_iter % C::NST;
           const uint32_t par = ((qd_iter / C::NST) & 1) ^ 1;
           uint8_t* q = sQD + st * 2 * C::TILE_BYTES;
-          const size_t row0 = (size_t)it.bh * p.Npad + (size_t)i * BQ;
+          const size_t row0 = row_of(it, i);
           uint8_t* ld = smem + C::OFF_LD + st * 1024;
-          ok = mbar_wait(&q_empty[st], par, w);
+          const int head = MODE == PACKED ? it.hk * p.pk.G + i.g : it.bh;
+          ok = await(&q_empty[st], par);
           if (!ok) break;
-          mbar_arrive_expect_tx(&q_full[st], C::TILE_BYTES + 512);
+          if (lead) {
+            mbar_arrive_expect_tx(&q_full[st], C::TILE_BYTES + 512);
 #pragma unroll
-          for (int c = 0; c < C::CHUNKS; ++c)
-            tma_load_3d(q + c * C::CHUNK_BYTES, &mapQ, &q_full[st], c * 64, i * BQ, it.bh);
-          // (a debug build that finds row0 out of range loads the first rows
-          // instead, so the barrier still gets its bytes)
-          bulk_load(ld, p.L2w + (FA_IN_BOUNDS(p.status, row0, 128, (size_t)p.BH * p.Npad) ? row0 : 0), 512,
-                    &q_full[st]);
-          ok = mbar_wait(&do_empty[st], par, w);
+            for (int c = 0; c < C::CHUNKS; ++c) load(q, &mapQ, &q_full[st], c, yq + i.i * BQ, it.sq, head);
+            // (a debug build that finds row0 out of range loads the first rows
+            // instead, so the barrier still gets its bytes)
+            bulk_load(ld, p.L2w + (FA_IN_BOUNDS(p.status, row0, 128, ws_rows) ? row0 : 0), 512, &q_full[st]);
+          }
+          ok = await(&do_empty[st], par);
           if (!ok) {
             ++qd_iter;
             q_only = true;
             break;
           }
-          mbar_arrive_expect_tx(&do_full[st], C::TILE_BYTES + 512);
+          if (lead) {
+            mbar_arrive_expect_tx(&do_full[st], C::TILE_BYTES + 512);
 #pragma unroll
-          for (int c = 0; c < C::CHUNKS; ++c)
-            tma_load_3d(q + C::TILE_BYTES + c * C::CHUNK_BYTES, &mapdO, &do_full[st], c * 64, i * BQ, it.bh);
-          bulk_load(ld + 512, p.Dw + (FA_IN_BOUNDS(p.status, row0, 128, (size_t)p.BH * p.Npad) ? row0 : 0), 512,
-                    &do_full[st]);
+            for (int c = 0; c < C::CHUNKS; ++c)
+              load(q + C::TILE_BYTES, &mapdO, &do_full[st], c, yq + i.i * BQ, it.sq, head);
+            bulk_load(ld + 512, p.Dw + (FA_IN_BOUNDS(p.status, row0, 128, ws_rows) ? row0 : 0), 512, &do_full[st]);
+          }
           ++qd_iter;
         }
         if (!ok) break;
@@ -500,13 +693,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
       for (;; ++item_iter) {
         int idx;
-        ok = take_item(item_iter, idx);
+        Item it;
+        ok = take_item(item_iter, idx, it);
         if (!ok || idx >= p.n_items) break;
-        const Item it = item_at<VARLEN>(p, idx);
         ok = mbar_wait(&kv_full, item_iter & 1, w);
         if (!ok) break;
-        int i = next_q<VARLEN>(p, it, 0);
-        if (i < p.nq) {
+        Step i = first_step<MODE>(p, it);
+        if (more<MODE>(p, it, i)) {
           ok = mbar_wait(&q_full[qd_iter % C::NST], (qd_iter / C::NST) & 1, w);
           if (!ok) break;
           tc_fence_after();
@@ -515,8 +708,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = issue_dp(qd_iter);
           if (!ok) break;
         }
-        for (int n = 0; ok && i < p.nq; ++n) {
-          const int inext = next_q<VARLEN>(p, it, i + 1);
+        for (int n = 0; ok && more<MODE>(p, it, i); ++n) {
+          const Step inext = next_step<MODE>(p, it, i);
+          const bool again = more<MODE>(p, it, inext);
           const uint32_t st = qd_iter % C::NST;         // stage of query tile i
           const uint32_t stn = (qd_iter + 1) % C::NST;  // stage of query tile inext
           const Desc gQ = desc_at(mQD, st * 2 * C::TILE_BYTES);  // MN-major Q of tile i
@@ -533,7 +727,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           // S^T of the next query tile goes in now: its columns were last read
           // by the dV product just issued, and its softmax can then overlap
           // the dK, dQ and next dP products.
-          if (inext < p.nq) {
+          if (again) {
             ok = mbar_wait(&q_full[stn], ((qd_iter + 1) / C::NST) & 1, w);
             if (!ok) break;
             tc_fence_after();
@@ -565,7 +759,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ++qd_iter;
           ++dq_iter;
           // dP^T of the next query tile (after the dQ drain when they share columns)
-          if (inext < p.nq) ok = issue_dp(qd_iter);
+          if (again) ok = issue_dp(qd_iter);
           i = inext;
         }
         if (!ok) break;
@@ -590,12 +784,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     for (uint32_t k = 0;; ++k) {
       int idx;
-      ok = take_item_warp(k, idx);
+      Item it;
+      ok = take_item_warp(k, idx, it);
       if (!ok || idx >= p.n_items) break;
-      const Item it = item_at<VARLEN>(p, idx);
       const int key = it.j * BK + kr;
       bool any = false;
-      for (int i = next_q<VARLEN>(p, it, 0); i < p.nq; i = next_q<VARLEN>(p, it, i + 1)) {
+      for (Step q = first_step<MODE>(p, it); more<MODE>(p, it, q); q = next_step<MODE>(p, it, q)) {
+        const int i = q.i;
         ok = mbar_wait_warp(&s_full, s_cnt & 1, w);
         if (!ok) break;
         const uint32_t par = s_cnt & 1;
@@ -607,12 +802,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const float* sD = sL + 128;
         // causal: query row q sees this key iff key <= q + off; some pair in
         // the tile is hidden iff its last key exceeds its first row's limit
-        const bool cmask = p.mask_kind == FA_MASK_CAUSAL && it.j * BK + BK - 1 > i * BQ + it.off;
+        // (PACKED: only on a tile's diagonal)
+        const bool cmask = p.mask_kind == FA_MASK_CAUSAL &&
+                           (MODE == PACKED ? it.j == i + it.off : it.j * BK + BK - 1 > i * BQ + it.off);
         // element masks only where the causal boundary or a ragged last key
         // tile crosses the tile: column c of this thread is hidden iff
         // c < kq, kq folding both tests (a missing key hides every column)
-        const bool masked = cmask || (it.j + 1) * BK > it.Lk;
-        const int kq = key >= it.Lk ? INT_MAX : (cmask ? key - (i * BQ + hf * 64 + it.off) : INT_MIN);
+        // (PACKED: the keys that a ragged tile lacks are its first, in tile 0)
+        const bool masked = cmask || (MODE == PACKED ? it.j == 0 && pack::pad(it.Lk) > 0 : (it.j + 1) * BK > it.Lk);
+        const bool no_key = MODE == PACKED ? key < pack::pad(it.Lk) : key >= it.Lk;
+        const int kq = no_key ? INT_MAX : (cmask ? (MODE == PACKED ? kr - hf * 64 : key - (i * BQ + hf * 64 + it.off)) : INT_MIN);
         // ---- P^T = exp2(S^T * scale * log2e - LSE_i * log2e), kept packed
         // as bf16 pairs (the form the dV product reads) for the dS step too.
         uint32_t pk[32];
@@ -704,12 +903,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!ok) break;
       ++dk_cnt;
       tc_fence_after();
-      const bool store = key < p.Nk;
+      const int prow = MODE == PACKED ? key - pack::pad(it.Lk) : key;  // PACKED: row of the sequence
+      const bool store = MODE == PACKED ? prow >= 0 : key < p.Nk;
       const size_t gbase = ((size_t)it.bh * p.Nk + key) * D;
+      // PACKED: rows leave one by one, in fp32, where their head has parts, and
+      // from a box that begins before the sequence
+      const bool parts = MODE == PACKED && p.part != nullptr;
+      const bool by_row = MODE == PACKED && (parts || prow - lane < 0);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {  // 0: dV, 1: dK
         const float mul = g == 0 ? 1.0f : p.scale;
-        __nv_bfloat16* dst = (g == 0 ? p.dV : p.dK) + gbase;
+        __nv_bfloat16* dst = (g == 0 ? p.dV : p.dK);
+        if (MODE == PACKED)
+          dst += (long long)(it.sk + prow) * (g == 0 ? p.dv_row : p.dk_row) + it.hk * (g == 0 ? p.dv_head : p.dk_head);
+        else
+          dst += gbase;
+        // fp32 row of this item's part
+        float* fdst = MODE == PACKED ? p.part + ((((long long)it.part * 2 + g) * p.pk.Tk + it.sk + prow) * p.pk.Hkv + it.hk) * D
+                                     : nullptr;
+        const bool row_ok = MODE != PACKED || FA_IN_BOUNDS(p.status, it.sk + prow, 1, p.pk.Tk);
         const int colbase = (g == 0 ? C::COL_DV : C::COL_DK) + hf * (D / 2);
         if constexpr (C::EPI_BYTES > 0) {
           // Lane i puts its 64 bytes (four 16-byte chunks, chunk c at slot
@@ -720,6 +932,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           uint32_t v[32];
           FA_TMEM_LD_X32(tmem + lane_bits + colbase, v);
           tc_wait_ld();
+          if (by_row) {
+            if (store && row_ok) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = any ? __uint_as_float(v[8 * c + e]) * mul : 0.0f;
+                if (parts) {
+                  float4* f = reinterpret_cast<float4*>(fdst + hf * 32 + 8 * c);
+                  f[0] = make_float4(o[0], o[1], o[2], o[3]);
+                  f[1] = make_float4(o[4], o[5], o[6], o[7]);
+                } else {
+                  *reinterpret_cast<uint4*>(dst + hf * 32 + 8 * c) =
+                      make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                 pack_bf16x2(o[6], o[7]));
+                }
+              }
+            }
+            continue;
+          }
           if (lane == 0) bulk_wait_read_all();  // the warp's previous store has read the buffer
           __syncwarp();
 #pragma unroll
@@ -736,7 +968,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           fence_proxy_async_smem();  // the generic-proxy writes, before the tensor store reads them
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(g == 0 ? &mapdV : &mapdK, ws, hf * 32, it.j * BK + quarter * 32, it.bh);
+            tma_store_3d(g == 0 ? &mapdV : &mapdK, ws, hf * 32, MODE == PACKED ? it.sk + prow : it.j * BK + quarter * 32,
+                         MODE == PACKED ? it.hk : it.bh);
             bulk_commit_group();
           }
         } else {
@@ -745,6 +978,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t v[32];
             FA_TMEM_LD_X32(tmem + lane_bits + colbase + c, v);
             tc_wait_ld();
+            if (parts) {
+              if (store && row_ok) {
+                float4* f = reinterpret_cast<float4*>(fdst + hf * (D / 2) + c);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  f[e] = any ? make_float4(__uint_as_float(v[4 * e]) * mul, __uint_as_float(v[4 * e + 1]) * mul,
+                                           __uint_as_float(v[4 * e + 2]) * mul, __uint_as_float(v[4 * e + 3]) * mul)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+              continue;
+            }
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -752,7 +996,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                           make_float2(mul, mul));
               pk[e] = any ? pack_bf16x2(o.x, o.y) : 0u;
             }
-            if (store && FA_IN_BOUNDS(p.status, gbase + hf * (D / 2) + c, 32, (size_t)p.BH * p.Nk * D)) {
+            if (store && row_ok &&
+                (MODE == PACKED || FA_IN_BOUNDS(p.status, gbase + hf * (D / 2) + c, 32, (size_t)p.BH * p.Nk * D))) {
               uint4* o = reinterpret_cast<uint4*>(dst + hf * (D / 2) + c);
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
@@ -778,10 +1023,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true, bulk_issued = false;
     for (uint32_t k = 0;; ++k) {
       int idx;
-      ok = take_item_warp(k, idx);
+      Item it;
+      ok = take_item_warp(k, idx, it);
       if (!ok || idx >= p.n_items) break;
-      const Item it = item_at<VARLEN>(p, idx);
-      for (int i = next_q<VARLEN>(p, it, 0); i < p.nq; i = next_q<VARLEN>(p, it, i + 1)) {
+      for (Step q = first_step<MODE>(p, it); more<MODE>(p, it, q); q = next_step<MODE>(p, it, q)) {
+        const size_t row0 = row_of(it, q);
         const uint32_t b = dq_iter % C::NDQ;
         const uint32_t st = dq_iter % C::NST;
         ok = mbar_wait_warp(&dq_full[b], (dq_iter / C::NDQ) & 1, w);
@@ -803,7 +1049,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // one bulk reduce-add (Cfg::DQ_PARTS).
         constexpr int GROUPS = D / 4 / C::DQ_PARTS;  // 4-column groups per part
         uint8_t* slot = sQD + st * 2 * C::TILE_BYTES + C::DQ_SLOT_OFF;
-        float* dst = p.dq_acc + ((size_t)it.bh * p.Npad + (size_t)i * BQ) * D;
+        float* dst = p.dq_acc + row0 * D;
         if (D == 128 && !p.deterministic) {
           // Both halves in flight at once: columns 64..127 staged in the dS
           // buffer (its dQ product has completed) and added first, columns
@@ -832,8 +1078,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mbar_arrive(&dq_staged[h]);
             if (leader) {
               ok = mbar_wait(&dq_staged[h], dq_iter & 1, w);
-              if (ok && FA_IN_BOUNDS(p.status, ((size_t)it.bh * p.Npad + (size_t)i * BQ) * D + part * GROUPS * 512,
-                                     C::DQ_PART_BYTES / 4, (size_t)p.BH * p.Npad * D))
+              if (ok && FA_IN_BOUNDS(p.status, row0 * D + part * GROUPS * 512, C::DQ_PART_BYTES / 4, ws_rows * D))
                 bulk_reduce_add_f32(dst + part * GROUPS * 512, buf, C::DQ_PART_BYTES);
               bulk_commit_group();
               bulk_issued = true;
@@ -875,16 +1120,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           mbar_arrive(&dq_staged[h]);
           if (leader) {
             ok = mbar_wait(&dq_staged[h], dq_iter & 1, w);
-            uint32_t* turn = p.turn + (size_t)it.bh * p.nq + i;
-            const bool turn_ok = !p.deterministic ||
-                                 FA_IN_BOUNDS(p.status, (size_t)it.bh * p.nq + i, 1, (size_t)p.BH * p.nq);
+            const size_t tile = row0 / BQ;
+            uint32_t* turn = p.turn + tile;
+            const bool turn_ok = !p.deterministic || FA_IN_BOUNDS(p.status, tile, 1, ws_rows / BQ);
             if (ok && p.deterministic && h == 0 && turn_ok) {
-              ok = wait_turn(turn, add_rank(p, it.j, i), w);
+              ok = wait_turn(turn, add_rank(p, it.j, q.i), w);
               fence_proxy_async_global();
             }
             if (ok) {
-              if (FA_IN_BOUNDS(p.status, ((size_t)it.bh * p.Npad + (size_t)i * BQ) * D + h * GROUPS * 512,
-                               C::DQ_PART_BYTES / 4, (size_t)p.BH * p.Npad * D))
+              if (FA_IN_BOUNDS(p.status, row0 * D + h * GROUPS * 512, C::DQ_PART_BYTES / 4, ws_rows * D))
                 bulk_reduce_add_f32(dst + h * GROUPS * 512, slot, C::DQ_PART_BYTES);
               bulk_commit_group();
               bulk_issued = true;
@@ -954,7 +1198,7 @@ static fa_status launch_bwd_d(const Problem& pr, const CUtensorMap& mQ, const CU
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   }
   if (stage < 0 || stage == 1) {
-    bwd::Params p;
+    bwd::Params p = {};
     p.BH = pr.BH;
     p.N = pr.N;
     p.Npad = Npad;
@@ -993,7 +1237,7 @@ static fa_status launch_bwd_d(const Problem& pr, const CUtensorMap& mQ, const CU
       return true;
     };
     const bool varlen = pr.seqlens_q || pr.seqlens_k;
-    if (!(varlen ? run(bwd::main_kernel<D, true>) : run(bwd::main_kernel<D, false>))) return FA_ERR_CUDA;
+    if (!(varlen ? run(bwd::main_kernel<D, PADDED>) : run(bwd::main_kernel<D, FIXED>))) return FA_ERR_CUDA;
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   }
   if (stage < 0 || stage == 2) {
@@ -1018,6 +1262,132 @@ fa_status launch_bwd(const Problem& pr, const void* Q, const void* K, const void
     return FA_ERR_CUDA;
   if (pr.d == 64) return launch_bwd_d<64>(pr, mQ, mK, mV, mdO, O, dO, LSE, dQ, dK, dV, workspace, s, st, stage);
   return launch_bwd_d<128>(pr, mQ, mK, mV, mdO, O, dO, LSE, dQ, dK, dV, workspace, s, st, stage);
+}
+
+// Parts that a key head's query heads are divided into: with fewer key tiles
+// than fill the GPU twice, more of them, so that grouped heads do not leave SMs
+// idle.  (Each part writes dK and dV in fp32, and the last kernel adds them.)
+static int packed_parts(const Pack& k) {
+  const long long items = (long long)(k.Tk / 128 + (k.B + 1) / 2) * k.Hkv;
+  const long long want = 2LL * num_sms();
+  if (k.G == 1 || items >= want || items == 0) return 1;
+  const long long n = (want + items - 1) / items;
+  return (int)(n < k.G ? n : k.G);
+}
+
+struct PackedWorkspace {
+  bwd::Workspace w;
+  size_t part_off, total;
+};
+static PackedWorkspace packed_layout(const Pack& k, int d) {
+  PackedWorkspace l;
+  l.w = bwd::workspace_layout(k.Hq, (int)pack::slots(k.Tq, k.B) * 128, d);
+  l.part_off = l.w.total;
+  const int parts = packed_parts(k);
+  l.total = l.part_off + (parts > 1 ? bwd::align256((size_t)parts * 2 * k.Tk * k.Hkv * d * sizeof(float)) : 0);
+  return l;
+}
+
+size_t bwd_packed_workspace_bytes(const Pack& k, int d) { return packed_layout(k, d).total; }
+
+template <int D>
+static fa_status launch_bwd_packed_d(const PackedProblem& pr, const CUtensorMap& mQ, const CUtensorMap& mK,
+                                     const CUtensorMap& mV, const CUtensorMap& mdO, const CUtensorMap& mdK,
+                                     const CUtensorMap& mdV, bwd::PackedArgs a, void* workspace, cudaStream_t s,
+                                     uint32_t* st) {
+  const Pack& k = pr.pk;
+  const PackedWorkspace l = packed_layout(k, D);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.pk = k;
+  a.dq_acc = reinterpret_cast<float*>(ws + l.w.dq_off);
+  a.Dw = reinterpret_cast<float*>(ws + l.w.d_off);
+  a.L2w = reinterpret_cast<float*>(ws + l.w.l2_off);
+  a.sched = reinterpret_cast<uint32_t*>(ws + l.w.sched_off);
+  a.turn = reinterpret_cast<uint32_t*>(ws + l.w.turn_off);
+  a.parts = packed_parts(k);
+  float* part = a.parts > 1 ? reinterpret_cast<float*>(ws + l.part_off) : nullptr;
+  a.part = part;
+  a.scale = pr.scale;
+  a.status = st;
+  const unsigned blocks = (unsigned)(pack::slots(k.Tq, k.B) * k.Hq);
+  bwd::packed_prep_kernel<D><<<blocks, 256, 0, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (k.Tk > 0) {
+    bwd::Params p = {};
+    p.pk = k;
+    p.d = D;
+    p.BH = k.Hq;
+    p.Npad = (int)pack::slots(k.Tq, k.B) * 128;
+    p.mask_kind = pr.mask_kind;
+    p.scale = pr.scale;
+    p.scale_log2 = pr.scale_log2;
+    p.Dw = a.Dw;
+    p.L2w = a.L2w;
+    p.dq_acc = a.dq_acc;
+    p.sched = a.sched;
+    p.turn = a.turn;
+    p.deterministic = pr.deterministic;
+    p.dK = a.dK;
+    p.dV = a.dV;
+    p.dk_row = a.dk_row;
+    p.dk_head = a.dk_head;
+    p.dv_row = a.dv_row;
+    p.dv_head = a.dv_head;
+    p.parts = a.parts;
+    p.part = part;
+    p.n_items = (int)(pack::slots(k.Tk, k.B) * k.Hkv * a.parts);  // at most
+    p.timeout_ns = wait_timeout_ns();
+    p.status = st;
+    constexpr int smem = bwd::Cfg<D>::SMEM_BYTES;
+    auto kern = bwd::main_kernel<D, PACKED>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FA_ERR_CUDA;
+    const int sms = num_sms();
+    kern<<<p.n_items < sms ? p.n_items : sms, bwd::NUM_THREADS, smem, s>>>(mQ, mK, mV, mdO, mdK, mdV, p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  }
+  const long long add = part ? ((long long)2 * k.Tk * k.Hkv * (D / 8) + 255) / 256 : 0;
+  const unsigned dq_blocks = k.Tq > 0 ? blocks : 0;
+  const unsigned more = (unsigned)(add < (1 << 20) ? add : (1 << 20));
+  if (dq_blocks + more > 0) bwd::packed_convert_kernel<D><<<dq_blocks + more, 256, 0, s>>>(a, dq_blocks);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status launch_bwd_packed(const PackedProblem& pr, const Rows& Q, const Rows& K, const Rows& V, const Rows& O,
+                            const Rows& dO, const float* LSE, const Rows& dQ, const Rows& dK, const Rows& dV,
+                            void* workspace, cudaStream_t s) {
+  uint32_t* st = status_word();
+  if (!st) return FA_ERR_CUDA;
+  const Pack& k = pr.pk;
+  // of tensors without rows nothing is read: their maps are another's
+  const bool q = k.Tq > 0, c = k.Tk > 0;
+  CUtensorMap mQ, mK, mV, mdO, mdK, mdV;
+  auto rows_map = [&](CUtensorMap* m, const Rows& r, bool query) {
+    if (query ? q : c) return make_map_packed(m, r, query ? k.Tq : k.Tk, query ? k.Hq : k.Hkv, pr.d);
+    return make_map_packed(m, query ? K : Q, query ? k.Tk : k.Tq, query ? k.Hkv : k.Hq, pr.d);
+  };
+  if (!rows_map(&mQ, Q, true) || !rows_map(&mdO, dO, true) || !rows_map(&mK, K, false) || !rows_map(&mV, V, false))
+    return FA_ERR_CUDA;
+  if (c ? !make_map_rows(&mdK, dK, k.Tk, k.Hkv, pr.d, 32, 32) || !make_map_rows(&mdV, dV, k.Tk, k.Hkv, pr.d, 32, 32) : false)
+    return FA_ERR_CUDA;
+  bwd::PackedArgs a = {};
+  a.O = static_cast<const __nv_bfloat16*>(O.data);
+  a.dO = static_cast<const __nv_bfloat16*>(dO.data);
+  a.o_row = O.row_stride;
+  a.o_head = O.head_stride;
+  a.do_row = dO.row_stride;
+  a.do_head = dO.head_stride;
+  a.LSE = LSE;
+  a.dQ = static_cast<__nv_bfloat16*>(dQ.data);
+  a.dK = static_cast<__nv_bfloat16*>(dK.data);
+  a.dV = static_cast<__nv_bfloat16*>(dV.data);
+  a.dq_row = dQ.row_stride;
+  a.dq_head = dQ.head_stride;
+  a.dk_row = dK.row_stride;
+  a.dk_head = dK.head_stride;
+  a.dv_row = dV.row_stride;
+  a.dv_head = dV.head_stride;
+  if (pr.d == 64) return launch_bwd_packed_d<64>(pr, mQ, mK, mV, mdO, mdK, mdV, a, workspace, s, st);
+  return launch_bwd_packed_d<128>(pr, mQ, mK, mV, mdO, mdK, mdV, a, workspace, s, st);
 }
 
 }  // namespace fa

@@ -109,9 +109,11 @@ struct Cfg {
   static_assert(REG_CTL + 2 * REG_SMX <= 3 * 168, "register split exceeds the launch");
 };
 
-// VARLEN: per-sequence lengths are read (else every sequence has N, Nk and
-// the sizes stay compile-time-free of extra registers).
-template <int D, bool VARLEN, int PIPES>
+// MODE: FIXED, every sequence has N, Nk (and the sizes stay compile-time-free
+// of extra registers); PADDED, per-sequence lengths are read; PACKED, packed
+// rows and grouped heads (the maps of Q, K and V then have a fourth dimension,
+// the head, behind the sequence's first row).
+template <int D, int MODE, int PIPES>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapO,
@@ -131,6 +133,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // A pipeline's producer claims work items and passes them to its other roles.
   __shared__ __align__(8) uint64_t item_full[2][RING], item_empty[2][RING];
   __shared__ int item_ring[2][RING];
+  // PACKED: the producer also passes on what it found the item to be
+  __shared__ int4 item_desc[2][MODE == PACKED ? RING : 1][2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
 
@@ -177,19 +181,39 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem = tmem_base_sh;
   const WaitCtx w{p.timeout_ns, &abort_flag, p.status};
 
-  auto take_item = [&](int q, uint32_t k, int& idx) -> bool {
+  // The k-th item of pipeline q; idx >= n_items: no more.
+  auto read_item = [&](int q, uint32_t slot, int& idx, Item& it) {
+    idx = *reinterpret_cast<volatile int*>(&item_ring[q][slot]);
+    if (MODE == PACKED) {
+      const int4 a = item_desc[q][slot][0], b = item_desc[q][slot][1];
+      it.q0 = a.x;
+      it.q1 = a.y & 0x7fffffff;
+      it.has1 = a.y < 0;
+      it.h0 = a.z;
+      it.h1 = a.w;
+      it.sq = b.x;
+      it.Lq = b.y;
+      it.sk = b.z;
+      it.Lk = b.w;
+      it.nkb = pack::tiles(it.Lk);
+      it.off = it.nkb - pack::tiles(it.Lq);
+    }
+  };
+  auto take_item = [&](int q, uint32_t k, int& idx, Item& it) -> bool {
     const uint32_t slot = k % RING;
     if (!mbar_wait(&item_full[q][slot], (k / RING) & 1, w)) return false;
-    idx = *reinterpret_cast<volatile int*>(&item_ring[q][slot]);
+    read_item(q, slot, idx, it);
     mbar_arrive(&item_empty[q][slot]);
+    if (MODE != PACKED && idx < p.n_items) it = item_at<MODE>(p, idx);
     return true;
   };
-  auto take_item_warp = [&](int q, uint32_t k, int& idx) -> bool {
+  auto take_item_warp = [&](int q, uint32_t k, int& idx, Item& it) -> bool {
     const uint32_t slot = k % RING;
     if (!mbar_wait_warp(&item_full[q][slot], (k / RING) & 1, w)) return false;
-    idx = *reinterpret_cast<volatile int*>(&item_ring[q][slot]);
+    read_item(q, slot, idx, it);
     __syncwarp();
     if (lane == 0) mbar_arrive(&item_empty[q][slot]);
+    if (MODE != PACKED && idx < p.n_items) it = item_at<MODE>(p, idx);
     return true;
   };
 
@@ -201,50 +225,83 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     regs_dec<C::REG_CTL>();  // may only lower the 168 registers of the launch
   if (warp == 0 || (C::DUAL && warp == 3)) {
     // ------------------------------------------------------------ producer
-    // (of pipeline q)
-    if (lane == 0) {
+    // (of pipeline q).  One thread; PACKED: the warp looks the items up
+    // together, and lane 0 issues the copies.
+    if (MODE == PACKED || lane == 0) {
       const int q = warp == 0 ? 0 : 1;
+      const bool lead = MODE != PACKED || lane == 0;
+      auto await = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return MODE == PACKED ? mbar_wait_warp(bar, parity, w) : mbar_wait(bar, parity, w);
+      };
+      // rows [y, y + 128) of a head's sequence (of head bh), 64 columns a copy
+      auto load = [&](uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int y, int start, int head) {
+#pragma unroll
+        for (int c = 0; c < C::CHUNKS; ++c) {
+          if (MODE == PACKED) tma_load_4d(dst + c * C::CHUNK_BYTES, m, bar, c * 64, y, start, head);
+          else tma_load_3d(dst + c * C::CHUNK_BYTES, m, bar, c * 64, y, head);
+        }
+      };
+      pack::Walker walk;
       uint32_t kv_iter = 0, item_iter = 0;
       bool q_loading = false;  // this item's Q load was issued
       bool ok = true;
       for (;; ++item_iter) {
         const uint32_t slot = item_iter % RING;
-        ok = mbar_wait(&item_empty[q][slot], ((item_iter / RING) & 1) ^ 1, w);
+        ok = await(&item_empty[q][slot], ((item_iter / RING) & 1) ^ 1);
         if (!ok) break;
         // Pipeline q of CTA b starts on item NPIPE b + q, then claims items
         // NPIPE gridDim.x, NPIPE gridDim.x + 1, ...
-        int idx = item_iter == 0 ? (int)(blockIdx.x * C::NPIPE) + q
-                                 : (int)(gridDim.x * C::NPIPE) + (int)atomicAdd(&g_claim[p.slot], 1u);
+        int idx = (int)(blockIdx.x * C::NPIPE) + q;
+        if (item_iter > 0) {
+          if (lead) idx = (int)(gridDim.x * C::NPIPE) + (int)atomicAdd(&g_claim[p.slot], 1u);
+          if (MODE == PACKED) idx = __shfl_sync(0xffffffffu, idx, 0);
+        }
         if (idx > p.n_items) idx = p.n_items;
-        item_ring[q][slot] = idx;
-        mbar_arrive(&item_full[q][slot]);
+        Item it;
+        if (MODE == PACKED) {
+          int b;
+          pack::Seq sq;
+          pack::Place at;
+          if (idx < p.n_items && pack::locate(p.pk, walk, idx, [&](const pack::Seq& x) { return packed_units(p, x); },
+                                              [](const pack::Seq& x) { return x.Lk; }, b, sq, at))
+            it = packed_item(p, sq, at);
+          else
+            idx = p.n_items;
+        } else if (idx < p.n_items) {
+          it = item_at<MODE>(p, idx);
+        }
+        if (lead) {
+          item_ring[q][slot] = idx;
+          if (MODE == PACKED && idx < p.n_items) {
+            item_desc[q][slot][0] = make_int4(it.q0, it.q1 | (it.has1 ? (int)0x80000000 : 0), it.h0, it.h1);
+            item_desc[q][slot][1] = make_int4(it.sq, it.Lq, it.sk, it.Lk);
+          }
+          mbar_arrive(&item_full[q][slot]);
+        }
         if (idx >= p.n_items) break;
-        const Item it = item_at<VARLEN>(p, idx);
         q_loading = false;
-        ok = mbar_wait(&q_empty[q], (item_iter & 1) ^ 1, w);
+        ok = await(&q_empty[q], (item_iter & 1) ^ 1);
         if (!ok) break;
-        mbar_arrive_expect_tx(&q_full[q], C::TILE_BYTES * (it.has1 ? 2 : 1));
-#pragma unroll
-        for (int c = 0; c < C::CHUNKS; ++c)
-          tma_load_3d(sQ + q * C::TILE_BYTES + c * C::CHUNK_BYTES, &mapQ, &q_full[q], c * 64, it.q0 * BM, it.bh);
-        if (it.has1) {
-#pragma unroll
-          for (int c = 0; c < C::CHUNKS; ++c)
-            tma_load_3d(sQ + C::TILE_BYTES + c * C::CHUNK_BYTES, &mapQ, &q_full[q], c * 64, it.q1 * BM, it.bh);
+        const int yq = MODE == PACKED ? -pack::pad(it.Lq) : 0, yk = MODE == PACKED ? -pack::pad(it.Lk) : 0;
+        const int hk = MODE == PACKED ? it.h0 / p.pk.G : it.bh;
+        if (lead) {
+          mbar_arrive_expect_tx(&q_full[q], C::TILE_BYTES * (it.has1 ? 2 : 1));
+          load(sQ + q * C::TILE_BYTES, &mapQ, &q_full[q], yq + it.q0 * BM, it.sq, MODE == PACKED ? it.h0 : it.bh);
+          if (it.has1)
+            load(sQ + C::TILE_BYTES, &mapQ, &q_full[q], yq + it.q1 * BM, it.sq, MODE == PACKED ? it.h1 : it.bh);
         }
         q_loading = true;
-        const int e = kv_end<VARLEN>(p, it);
-        for (int j = next_union<VARLEN>(p, it, 0); ok && j < e; j = next_union<VARLEN>(p, it, j + 1)) {
+        const int e = kv_end<MODE>(p, it);
+        for (int j = next_union<MODE>(p, it, 0); ok && j < e; j = next_union<MODE>(p, it, j + 1)) {
           for (int kv = 0; kv < 2; ++kv) {
             const uint32_t slot = kv_iter % C::NSLOT;
-            ok = mbar_wait(&kv_empty[q][slot], ((kv_iter / C::NSLOT) & 1) ^ 1, w);
+            ok = await(&kv_empty[q][slot], ((kv_iter / C::NSLOT) & 1) ^ 1);
             if (!ok) break;
-            mbar_arrive_expect_tx(&kv_full[q][slot], C::TILE_BYTES);
-            uint8_t* dst = sKV + (q * C::NSLOT + slot) * C::TILE_BYTES;
-            const CUtensorMap* m = kv == 0 ? &mapK : &mapV;
-#pragma unroll
-            for (int c = 0; c < C::CHUNKS; ++c)
-              tma_load_3d(dst + c * C::CHUNK_BYTES, m, &kv_full[q][slot], c * 64, j * BN, it.bh);
+            if (lead) {
+              mbar_arrive_expect_tx(&kv_full[q][slot], C::TILE_BYTES);
+              load(sKV + (q * C::NSLOT + slot) * C::TILE_BYTES, kv == 0 ? &mapK : &mapV, &kv_full[q][slot], yk + j * BN,
+                   it.sk, hk);
+            }
             ++kv_iter;
           }
         }
@@ -253,7 +310,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // This pipeline claims no more (its last claim ran past the end, or it
       // aborted); the last pipeline of the launch to get here resets the
       // counter slot.
-      if (atomicAdd(&g_done[p.slot], 1u) == gridDim.x * C::NPIPE - 1) {
+      if (lead && atomicAdd(&g_done[p.slot], 1u) == gridDim.x * C::NPIPE - 1) {
         g_claim[p.slot] = 0u;
         g_done[p.slot] = 0u;
       }
@@ -328,26 +385,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t s_iss = 0, pv_iss = 0;
         for (;; ++item_iter) {
           int idx;
-          ok = take_item(q, item_iter, idx);
+          Item it;
+          ok = take_item(q, item_iter, idx, it);
           if (!ok || idx >= p.n_items) break;
-          const Item it = item_at<VARLEN>(p, idx);
           const bool mine = C::DUAL || t == 0 || it.has1;
           const int qt = (C::DUAL || t == 0) ? it.q0 : it.q1;
           ok = mbar_wait(&q_full[q], item_iter & 1, w);
           if (!ok) break;
           tc_fence_after();
-          const int e = kv_end<VARLEN>(p, it);
-          int j = next_union<VARLEN>(p, it, 0), jp = -1;
+          const int e = kv_end<MODE>(p, it);
+          int j = next_union<MODE>(p, it, 0), jp = -1;
           if (j >= e) tc_commit(&q_empty[q]);  // no key tile: Q was not read
           bool first_pv = true;
           while (ok && (j < e || jp >= 0)) {
-            const int jn = j < e ? next_union<VARLEN>(p, it, j + 1) : e;
+            const int jn = j < e ? next_union<MODE>(p, it, j + 1) : e;
             if (j < e) {
               const uint32_t ks = kv_iter % C::NSLOT;
               ok = mbar_wait(&kv_full[q][ks], (kv_iter / C::NSLOT) & 1, w);
               if (!ok) break;
               tc_fence_after();
-              if (mine && member<VARLEN>(p, it, qt, j)) {
+              if (mine && member<MODE>(p, it, qt, j)) {
                 if (s_iss > 0) {
                   ok = mbar_wait(&s_free[t], (s_iss - 1) & 1, w);
                   if (!ok) break;
@@ -364,7 +421,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               ok = mbar_wait(&kv_full[q][vs], (vi / C::NSLOT) & 1, w);
               if (!ok) break;
               tc_fence_after();
-              if (mine && member<VARLEN>(p, it, qt, jp)) {
+              if (mine && member<MODE>(p, it, qt, jp)) {
                 ok = mbar_wait(&p_full[t], pv_iss & 1, w);
                 if (!ok) break;
                 tc_fence_after();
@@ -384,16 +441,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       } else {
       for (;; ++item_iter) {
         int idx;
-        ok = take_item(0, item_iter, idx);
+        Item it;
+        ok = take_item(0, item_iter, idx, it);
         if (!ok || idx >= p.n_items) break;
-        const Item it = item_at<VARLEN>(p, idx);
         const int tiles = it.has1 ? 2 : 1;  // tiles [0, tiles) exist
         ok = mbar_wait(&q_full[0], item_iter & 1, w);
         if (!ok) break;
         tc_fence_after();
-        const int e = kv_end<VARLEN>(p, it);
-        int j = next_union<VARLEN>(p, it, 0);
-        int jn = j < e ? next_union<VARLEN>(p, it, j + 1) : e;  // the key tile after j
+        const int e = kv_end<MODE>(p, it);
+        int j = next_union<MODE>(p, it, 0);
+        int jn = j < e ? next_union<MODE>(p, it, j + 1) : e;  // the key tile after j
         bool first_pv[2] = {true, true};
         // Q is read only by the QK^T products: it goes back to the producer
         // once the item's last one has been issued, so the next item's Q
@@ -405,7 +462,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
           tc_fence_after();
           for (int t = t_lo; t < t_hi && t < tiles; ++t)
-            if (member<VARLEN>(p, it, t == 0 ? it.q0 : it.q1, j)) issue_s(t, ks);
+            if (member<MODE>(p, it, t == 0 ? it.q0 : it.q1, j)) issue_s(t, ks);
           tc_commit(&kv_empty[0][ks]);
           ++kv_iter;
           if (jn >= e) {
@@ -414,7 +471,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
         while (ok && j < e) {
-          const int jnn = jn < e ? next_union<VARLEN>(p, it, jn + 1) : e;
+          const int jnn = jn < e ? next_union<MODE>(p, it, jn + 1) : e;
           const uint32_t vs = kv_iter % C::NSLOT;
           const uint32_t ksn = (kv_iter + 1) % C::NSLOT;
           ok = mbar_wait(&kv_full[0][vs], (kv_iter / C::NSLOT) & 1, w);
@@ -423,7 +480,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tc_fence_after();
           for (int t = t_lo; t < t_hi && t < tiles && ok; ++t) {
             const int qt = t == 0 ? it.q0 : it.q1;
-            if (member<VARLEN>(p, it, qt, j)) {
+            if (member<MODE>(p, it, qt, j)) {
               ok = mbar_wait(&p_full[t], p_cnt[t] & 1, w);
               if (!ok) break;
               ++p_cnt[t];
@@ -431,7 +488,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               issue_pv(t, vs, first_pv[t] ? 0u : 1u);
               first_pv[t] = false;
             }
-            if (jn < e && member<VARLEN>(p, it, qt, jn)) issue_s(t, ksn);
+            if (jn < e && member<MODE>(p, it, qt, jn)) issue_s(t, ksn);
           }
           if (!ok) break;
           tc_commit(&kv_empty[0][vs]);
@@ -479,16 +536,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
     for (uint32_t k = 0;; ++k) {
       int idx;
-      ok = take_item_warp(C::DUAL ? t : 0, k, idx);
+      Item it;
+      ok = take_item_warp(C::DUAL ? t : 0, k, idx, it);
       if (!ok || idx >= p.n_items) break;
-      const Item it = item_at<VARLEN>(p, idx);
       if (!C::DUAL && t == 1 && !it.has1) continue;
       const int qt = (C::DUAL || t == 0) ? it.q0 : it.q1;  // DUAL: each pipeline's item is one tile
       const int row = qt * BM + r;
       float m = -INFINITY;  // reference maximum, scaled log2 units
       float l = 0.0f;
       bool first = true;  // no PV has written this tile's O yet
-      const int e = kv_end<VARLEN>(p, it);
+      const int e = kv_end<MODE>(p, it);
       // The key tiles this query tile visits, in order.  Under a block mask
       // the warp reads its row of the mask 32 key tiles at a time (one byte a
       // lane, then a ballot) instead of one dependent load per key tile.
@@ -496,14 +553,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int mbase = -64;  // first key tile of the 32 in mbits
       auto next_key = [&](int j) -> int {
         if (p.mask_kind != FA_MASK_BLOCK) {
-          while (j < e && !member<VARLEN>(p, it, qt, j)) ++j;
+          while (j < e && !member<MODE>(p, it, qt, j)) ++j;
           return j < e ? j : e;
         }
         while (j < e) {
           if (j < mbase || j >= mbase + 32) {
             mbase = j & ~31;
             const int jj = mbase + lane;
-            mbits = __ballot_sync(0xffffffffu, jj < e && member<VARLEN>(p, it, qt, jj));
+            mbits = __ballot_sync(0xffffffffu, jj < e && member<MODE>(p, it, qt, jj));
           }
           const uint32_t rest = mbits >> (j - mbase);
           if (rest) return j + __ffs(rest) - 1;
@@ -530,8 +587,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // valid columns [0, lim): keys that exist and, under the causal mask,
         // keys <= row + off
         const int key0 = j * BN;
-        int lim = min(BN, it.Lk - key0);
-        if (p.mask_kind == FA_MASK_CAUSAL) lim = max(0, min(lim, row + it.off + 1 - key0));
+        int lim;
+        if (MODE == PACKED) {
+          // tiles counted from the end: the causal boundary is a tile's
+          // diagonal, and the columns before the first key are in tile 0
+          lim = p.mask_kind == FA_MASK_CAUSAL && j == qt + it.off ? r + 1 : BN;
+          const int lo = j == 0 ? pack::pad(it.Lk) : 0;
+          if (lo > 0) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+              if (c < lo) x[c] = -INFINITY;
+          }
+        } else {
+          lim = min(BN, it.Lk - key0);
+          if (p.mask_kind == FA_MASK_CAUSAL) lim = max(0, min(lim, row + it.off + 1 - key0));
+        }
         if (lim < BN) {
 #pragma unroll
           for (int c = 0; c < BN; ++c)
@@ -637,7 +707,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
       tc_fence_after();
-      const bool live = l > 0.0f && row < it.Lq;  // false for a row that sees no key, or padding
+      // false for a row that sees no key, or padding
+      // (PACKED: a NaN that a row saw is kept)
+      const bool live = MODE == PACKED ? l != 0.0f : l > 0.0f && row < it.Lq;
+      // PACKED: the row's place in the packed tensors (negative: before the
+      // sequence), and its head
+      const int prow = MODE == PACKED ? row - pack::pad(it.Lq) : 0;
+      const int head = MODE == PACKED ? ((C::DUAL || t == 0) ? it.h0 : it.h1) : it.bh;
       const float inv_l = live ? 1.0f / l : 0.0f;
       {
         // Per 64 columns: lane i puts row i of the warp's 32 (128 bytes:
@@ -645,7 +721,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // 128-byte swizzle), then lane 0 stores the 32 x 64 box with one
         // tensor store (rows past N are not written).
         uint8_t* ws = sO + (warp - 4) * 4096;
-        const int row0 = qt * BM + quarter * 32;
+        const int row0 = MODE == PACKED ? it.sq + prow - lane : qt * BM + quarter * 32;
+        // PACKED: a box that begins before the sequence leaves row by row (a
+        // tensor store would write the rows of the sequence before)
+        const bool by_row = MODE == PACKED && prow - lane < 0;
 #pragma unroll
         for (int g = 0; g < D / 64; ++g) {
           if (lane == 0) bulk_wait_read_all();  // the warp's previous store has read the buffer
@@ -662,6 +741,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                           make_float2(inv_l, inv_l));
               pk[i] = live ? pack_bf16x2(o.x, o.y) : 0u;
             }
+            if (by_row) {
+              const long long at = (long long)(it.sq + prow) * p.o_row + head * p.o_head + 64 * g + c;
+              if (prow >= 0 && FA_IN_BOUNDS(p.status, it.sq + prow, 1, p.pk.Tq)) {
+                uint4* o = reinterpret_cast<uint4*>(p.O + at);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+              }
+              continue;
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int k = c / 8 + i;
@@ -671,13 +759,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           fence_proxy_async_smem();  // the generic-proxy writes, before the tensor store reads them
           __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&mapO, ws, 64 * g, row0, it.bh);
+          if (lane == 0 && !by_row) {
+            tma_store_3d(&mapO, ws, 64 * g, row0, head);
             bulk_commit_group();
           }
         }
       }
-      if (row < p.N && FA_IN_BOUNDS(p.status, (size_t)it.bh * p.N + row, 1, (size_t)p.BH * p.N))
+      if (MODE == PACKED) {
+        const size_t at = (size_t)head * p.pk.Tq + it.sq + prow;
+        if (prow >= 0 && FA_IN_BOUNDS(p.status, at, 1, (size_t)p.pk.Hq * p.pk.Tq))
+          p.LSE[at] = live ? (m + log2f(l)) * LN2 : -INFINITY;
+      } else if (row < p.N && FA_IN_BOUNDS(p.status, (size_t)it.bh * p.N + row, 1, (size_t)p.BH * p.N))
         p.LSE[(size_t)it.bh * p.N + row] = live ? (m + log2f(l)) * LN2 : -INFINITY;
       tc_fence_before();
     }
@@ -691,6 +783,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// The counter slot of the next launch.
+static uint32_t next_slot() {
+  static std::atomic<uint32_t> next{0};
+  return next.fetch_add(1u, std::memory_order_relaxed) % SCHED_SLOTS;
 }
 
 }  // namespace fwd
@@ -726,8 +824,7 @@ fa_status launch_fwd(const Problem& pr, const void* Q, const void* K, const void
   p.LSE = LSE;
   p.timeout_ns = wait_timeout_ns();
   p.status = st;
-  static std::atomic<uint32_t> next_slot{0};
-  p.slot = next_slot.fetch_add(1u, std::memory_order_relaxed) % fwd::SCHED_SLOTS;
+  p.slot = fwd::next_slot();
   const int npipe = dual ? 2 : 1;
   const int want = (p.n_items + npipe - 1) / npipe;  // CTAs that get a first item in every pipeline
   const int grid = want < num_sms() ? want : num_sms();
@@ -739,12 +836,55 @@ fa_status launch_fwd(const Problem& pr, const void* Q, const void* K, const void
   const bool varlen = pr.seqlens_q || pr.seqlens_k;
   bool ok;
   if (dual)
-    ok = varlen ? run(fwd::fwd_kernel<64, true, 2>, fwd::Cfg<64, 2>::SMEM_BYTES)
-                : run(fwd::fwd_kernel<64, false, 2>, fwd::Cfg<64, 2>::SMEM_BYTES);
+    ok = varlen ? run(fwd::fwd_kernel<64, PADDED, 2>, fwd::Cfg<64, 2>::SMEM_BYTES)
+                : run(fwd::fwd_kernel<64, FIXED, 2>, fwd::Cfg<64, 2>::SMEM_BYTES);
   else
-    ok = varlen ? run(fwd::fwd_kernel<128, true, 1>, fwd::Cfg<128, 1>::SMEM_BYTES)
-                : run(fwd::fwd_kernel<128, false, 1>, fwd::Cfg<128, 1>::SMEM_BYTES);
+    ok = varlen ? run(fwd::fwd_kernel<128, PADDED, 1>, fwd::Cfg<128, 1>::SMEM_BYTES)
+                : run(fwd::fwd_kernel<128, FIXED, 1>, fwd::Cfg<128, 1>::SMEM_BYTES);
   if (!ok) return FA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status launch_fwd_packed(const PackedProblem& pr, const Rows& Q, const Rows& K, const Rows& V, const Rows& O,
+                            float* LSE, cudaStream_t s) {
+  uint32_t* st = status_word();
+  if (!st) return FA_ERR_CUDA;
+  const Pack& k = pr.pk;
+  CUtensorMap mQ, mK, mV, mO;
+  // without a key nothing is read of K and V: their maps are Q's
+  const bool keys = k.Tk > 0;
+  if (!make_map_packed(&mQ, Q, k.Tq, k.Hq, pr.d) || !make_map_packed(&mK, keys ? K : Q, keys ? k.Tk : k.Tq, keys ? k.Hkv : k.Hq, pr.d) ||
+      !make_map_packed(&mV, keys ? V : Q, keys ? k.Tk : k.Tq, keys ? k.Hkv : k.Hq, pr.d) ||
+      !make_map_rows(&mO, O, k.Tq, k.Hq, pr.d, 64, 32))
+    return FA_ERR_CUDA;
+  fwd::Params p = {};
+  p.pk = k;
+  p.d = pr.d;
+  const bool dual = pr.d == 64;
+  p.tiles_per_item = dual ? 1 : 2;
+  p.by_heads = !dual && k.G % 2 == 0;
+  // at most: the sequences' tiles number no more than the slots
+  p.n_items = (int)(pack::slots(k.Tq, k.B) * (p.by_heads ? k.Hq / 2 : k.Hq));
+  p.mask_kind = pr.mask_kind;
+  p.scale_log2 = pr.scale_log2;
+  p.O = static_cast<__nv_bfloat16*>(O.data);
+  p.o_row = O.row_stride;
+  p.o_head = O.head_stride;
+  p.LSE = LSE;
+  p.timeout_ns = wait_timeout_ns();
+  p.status = st;
+  p.slot = fwd::next_slot();
+  const int npipe = dual ? 2 : 1;
+  const int want = (p.n_items + npipe - 1) / npipe;
+  const int grid = want < num_sms() ? want : num_sms();
+  auto run = [&](auto kern, int smem) -> bool {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+    kern<<<grid, fwd::NUM_THREADS, smem, s>>>(mQ, mK, mV, mO, p);
+    return true;
+  };
+  if (!(dual ? run(fwd::fwd_kernel<64, PACKED, 2>, fwd::Cfg<64, 2>::SMEM_BYTES)
+             : run(fwd::fwd_kernel<128, PACKED, 1>, fwd::Cfg<128, 1>::SMEM_BYTES)))
+    return FA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "fa.h"
+#include "pack.cuh"
 
 namespace fa {
 
@@ -26,6 +27,20 @@ struct Problem {
   float scale_log2;  // scale * log2(e), computed in double and rounded once
 };
 
+// Rows of a packed tensor [rows, heads, d]; strides in elements.
+struct Rows {
+  void* data;
+  long long row_stride, head_stride;
+};
+
+// Packed sequences after validation.
+struct PackedProblem {
+  Pack pk;
+  int d, mask_kind;
+  int deterministic = 0;
+  float scale, scale_log2;
+};
+
 // Encode a 3-D tiled TMA map over a contiguous bf16 [BH, N, d] tensor:
 // dims (d, N, BH), box (64, box_rows, 1), 128-byte swizzle, zero fill out of
 // bounds.  Returns false on failure.
@@ -33,6 +48,12 @@ bool make_map_bf16(CUtensorMap* map, const void* base, int BH, int N, int d, int
 // The same [BH, N, d] view with a box of box_cols (32 or 64) x box_rows and the
 // swizzle of the box's row width (64 or 128 bytes): for tiled stores.
 bool make_map_bf16_box(CUtensorMap* map, const void* base, int BH, int N, int d, int box_cols, int box_rows);
+
+// Rows [T, heads, d] as (d, T, heads), box box_cols x box_rows x 1: for tiled stores.
+bool make_map_rows(CUtensorMap* map, const Rows& r, int T, int heads, int d, int box_cols, int box_rows);
+// Rows [T, heads, d] as (d, row of the sequence, first row of the sequence,
+// heads), box 64 x 128 x 1 x 1 (pack.cuh): for loads.
+bool make_map_packed(CUtensorMap* map, const Rows& r, int T, int heads, int d);
 
 // Same for a 2-D row-major bf16 matrix [rows, cols] (used by the self-test).
 bool make_map_bf16_2d(CUtensorMap* map, const void* base, int rows, int cols, int box_rows);
@@ -45,11 +66,17 @@ int num_sms();
 // Kernel launchers (defined next to their kernels).
 fa_status launch_fwd(const Problem& p, const void* Q, const void* K, const void* V, void* O, float* LSE,
                      cudaStream_t s);
+fa_status launch_fwd_packed(const PackedProblem& p, const Rows& Q, const Rows& K, const Rows& V, const Rows& O,
+                            float* LSE, cudaStream_t s);
 // stage < 0: all three stages; otherwise only the given one (0, 1 or 2).
 fa_status launch_bwd(const Problem& p, const void* Q, const void* K, const void* V, const void* O,
                      const void* dO, const float* LSE, void* dQ, void* dK, void* dV, void* workspace,
                      cudaStream_t s, int stage);
 size_t bwd_workspace_bytes(int B, int H, int N, int d);
+size_t bwd_packed_workspace_bytes(const Pack& k, int d);
+fa_status launch_bwd_packed(const PackedProblem& p, const Rows& Q, const Rows& K, const Rows& V, const Rows& O,
+                            const Rows& dO, const float* LSE, const Rows& dQ, const Rows& dK, const Rows& dV,
+                            void* workspace, cudaStream_t s);
 // Decode (few queries, long key history): workspace for the split-key
 // partial results on the current device (0 on failure), and the launch.
 size_t decode_workspace_bytes(int BH, int Nq, int Nk, int d);
@@ -60,12 +87,6 @@ fa_status launch_decode(const Problem& p, const void* Q, const void* K, const vo
 size_t standard_workspace_bytes(int BH, int N);
 fa_status launch_standard_fwd(const Problem& p, const void* Q, const void* K, const void* V, void* O, float* LSE,
                               void* workspace, cudaStream_t s);
-// Rows of a packed tensor [rows, heads, d]; strides in elements.
-struct Rows {
-  void* data;
-  long long row_stride, head_stride;
-};
-
 // A paged cache after validation (strides in elements; elem: bytes of one).
 struct PagedCache {
   void* K;

@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include "fa.h"
+#include "pack.cuh"
 #include "sm100.cuh"
 
 namespace fa {
@@ -36,6 +37,10 @@ struct Params {
   uint64_t timeout_ns;
   uint32_t* status;
   uint32_t slot;  // scheduler counter slot of this launch
+  Pack pk;        // packed sequences (PACKED)
+  int by_heads;   // PACKED: an item's two tiles are two heads' of one query tile
+  int d;
+  long long o_row, o_head;  // PACKED: strides of O, elements
 };
 
 // Heads per scheduling group.  The group's K and V tiles are the forward's
@@ -54,6 +59,9 @@ struct Item {
   int bh, q0, q1;
   bool has1;
   int Lq, Lk, off, nkb;  // this sequence's query rows and keys, causal offset, key tiles
+  // PACKED: the heads of the item's tiles, the sequence's first query row and
+  // key; off counts tiles.
+  int h0, h1, sq, sk;
 };
 
 // Work item idx -> (head, pair of query tiles, or one query tile).  Heads are taken in groups
@@ -61,7 +69,7 @@ struct Item {
 // in L2; within a group later query tiles come first, so that under a causal
 // mask the longest items start earliest (and, claimed dynamically, the short
 // ones fill in at the end).
-template <bool VARLEN>
+template <int MODE>
 __host__ __device__ __forceinline__ Item item_at(const Params& p, int idx) {
   Item it;
   const int per_group = p.group * p.n_pairs;
@@ -72,7 +80,7 @@ __host__ __device__ __forceinline__ Item item_at(const Params& p, int idx) {
   it.q0 = p.tiles_per_item * c;
   it.q1 = it.q0 + 1;
   it.has1 = p.tiles_per_item == 2 && it.q1 < p.nq;
-  if (VARLEN) {
+  if (MODE == PADDED) {
     const int b = it.bh / p.H;
     const bool bok = FA_IN_BOUNDS(p.status, b, 1, p.BH / p.H);
     it.Lq = p.seqlens_q ? (bok ? min(max(ld_ro(p.seqlens_q + b), 0), p.N) : 0) : p.N;
@@ -88,6 +96,46 @@ __host__ __device__ __forceinline__ Item item_at(const Params& p, int idx) {
   return it;
 }
 
+// Packed sequences.  An item's one or two query tiles: at d = 64 one; at
+// d = 128 one query tile of two heads that share their keys where the heads of
+// a key head come in pairs (both see the same keys, and a sequence of one tile
+// still fills the item), else two neighbouring tiles, from the end.
+__host__ __device__ __forceinline__ pack::Units packed_units(const Params& p, const pack::Seq& s) {
+  pack::Units u;
+  const int nq = pack::tiles(s.Lq), per = p.by_heads ? 2 : 1;
+  u.tiles = p.tiles_per_item == 2 && !p.by_heads ? (nq + 1) / 2 : nq;
+  u.heads = p.pk.Hq / per;
+  // the heads of whole key heads, their K and V kept to about 32 MiB (as sched_group)
+  const long long fit = (32LL << 20) / (4LL * max(s.Lk, 1) * p.d);
+  const long long least = (8 + p.pk.G - 1) / p.pk.G;  // 8 query heads
+  u.group = (int)min((long long)p.pk.Hkv, max(fit, least)) * p.pk.G / per;
+  return u;
+}
+
+__host__ __device__ __forceinline__ Item packed_item(const Params& p, const pack::Seq& s, const pack::Place& at) {
+  Item it;
+  const int nq = pack::tiles(s.Lq);
+  it.bh = 0;
+  it.Lq = s.Lq;
+  it.Lk = s.Lk;
+  it.nkb = pack::tiles(s.Lk);
+  it.off = it.nkb - nq;
+  it.sq = s.sq;
+  it.sk = s.sk;
+  if (p.tiles_per_item == 1 || p.by_heads) {
+    it.q0 = it.q1 = nq - 1 - at.tile;
+    it.has1 = p.by_heads;
+    it.h0 = p.by_heads ? 2 * at.head : at.head;
+    it.h1 = it.h0 + 1;
+  } else {
+    it.h0 = it.h1 = at.head;
+    it.q1 = nq - 1 - 2 * at.tile;
+    it.has1 = it.q1 > 0;
+    it.q0 = it.has1 ? it.q1 - 1 : 0;
+  }
+  return it;
+}
+
 // Last key a query row of tile qt may see under the causal mask (the tile's
 // last row of the sequence, shifted by the alignment; negative: none).
 __host__ __device__ __forceinline__ int causal_last_key(const Item& it, int qt) {
@@ -97,9 +145,10 @@ __host__ __device__ __forceinline__ int causal_last_key(const Item& it, int qt) 
 // Does query tile qt attend to key tile j?  (With per-sequence lengths,
 // tiles past the sequence's query rows or keys attend to nothing; without,
 // every tile an item or a key loop reaches is inside.)
-template <bool VARLEN>
+template <int MODE>
 __host__ __device__ __forceinline__ bool member(const Params& p, const Item& it, int qt, int j) {
-  if (VARLEN && (qt * BM >= it.Lq || j >= it.nkb)) return false;
+  if (MODE == PADDED && (qt * BM >= it.Lq || j >= it.nkb)) return false;
+  if (MODE == PACKED) return j < it.nkb && (p.mask_kind != FA_MASK_CAUSAL || j <= qt + it.off);
   if (p.mask_kind == FA_MASK_CAUSAL) return j * BN <= causal_last_key(it, qt);
   if (p.mask_kind == FA_MASK_BLOCK)
     return FA_IN_BOUNDS(p.status, (size_t)qt * p.nk + j, 1, (size_t)p.nq * p.nk) &&
@@ -108,23 +157,25 @@ __host__ __device__ __forceinline__ bool member(const Params& p, const Item& it,
 }
 
 // One past the last key tile either query tile of the item may need.
-template <bool VARLEN>
+template <int MODE>
 __host__ __device__ __forceinline__ int kv_end(const Params& p, const Item& it) {
-  if (VARLEN && it.q0 * BM >= it.Lq) return 0;
+  if (MODE == PADDED && it.q0 * BM >= it.Lq) return 0;
+  if (MODE == PACKED)
+    return p.mask_kind == FA_MASK_CAUSAL ? max(0, min(it.nkb, (it.has1 ? it.q1 : it.q0) + it.off + 1)) : it.nkb;
   if (p.mask_kind == FA_MASK_CAUSAL) {
-    const int last = causal_last_key(it, (it.has1 && (!VARLEN || it.q1 * BM < it.Lq)) ? it.q1 : it.q0);
+    const int last = causal_last_key(it, (it.has1 && (MODE != PADDED || it.q1 * BM < it.Lq)) ? it.q1 : it.q0);
     return last < 0 ? 0 : min(it.nkb, last / BN + 1);
   }
   return it.nkb;
 }
 
 // Next key tile >= j needed by either query tile of the item (kv_end if none).
-template <bool VARLEN>
+template <int MODE>
 __host__ __device__ __forceinline__ int next_union(const Params& p, const Item& it, int j) {
-  const int e = kv_end<VARLEN>(p, it);
+  const int e = kv_end<MODE>(p, it);
   if (p.mask_kind != FA_MASK_BLOCK) return j < e ? j : e;
   for (; j < e; ++j)
-    if (member<VARLEN>(p, it, it.q0, j) || (it.has1 && member<VARLEN>(p, it, it.q1, j))) return j;
+    if (member<MODE>(p, it, it.q0, j) || (it.has1 && member<MODE>(p, it, it.q1, j))) return j;
   return e;
 }
 

@@ -201,6 +201,47 @@ fa_status fa_decode(const void* Q, const void* K, const void* V, int B, int H, i
                     int mask_kind, float scale, void* O, float* LSE, void* workspace,
                     size_t workspace_bytes, void* stream);
 
+/* ---- Packed sequences, grouped heads ----------------------------------------
+ * Rows [rows, heads, d] of bf16 (one row a token), d contiguous, 16-byte
+ * aligned; strides in elements, multiples of 8: a slice of a fused projection
+ * needs no copy. */
+typedef struct {
+  void* data;
+  int64_t row_stride, head_stride;
+} fa_rows;
+
+/* Sequences of different lengths one behind the other, without padding: sequence
+ * b owns rows [cu_q[b], cu_q[b+1]) of Q, O, dO and dQ and rows [cu_k[b], cu_k[b+1])
+ * of K, V, dK and dV (cu_q, cu_k: DEVICE int [B+1], ascending from 0 or more).
+ * Each is its own attention problem, as in fa_fwd_varlen; causal is aligned at
+ * the bottom right of each (query i sees keys j <= i + Lk - Lq).  Query head h
+ * reads key head h / (Hq / Hkv), Hq a multiple of Hkv.  Lengths may be zero; a row
+ * without a visible key gets O = 0, LSE = -inf and no gradient, a key that no
+ * query sees zero gradients.  No row of another sequence, or that belongs to
+ * none, has any effect, whatever it holds; output rows that belong to no sequence
+ * are left as they were.  Entries of cu outside the tensors are held to them.
+ * In:  Q, O, dO, dQ: Tq rows of Hq heads; K, V, dK, dV: Tk rows of Hkv heads
+ *      (strides above 0; of a tensor without rows nothing is used); LSE: fp32
+ *      [Hq, Tq]; mask_kind FA_MASK_NONE or FA_MASK_CAUSAL; scale > 0; workspace
+ *      (DEVICE, 256-byte aligned, of the given size for the same arguments,
+ *      contents irrelevant on entry; calls that may overlap need one each).
+ * Out: fa_fwd_packed: O, LSE; fa_bwd_packed: dQ, dK, dV.  The gradients of a key
+ *      head are summed over its query heads in fp32 and rounded once.  dK and dV
+ *      have the same bits on every run, dQ with deterministic != 0 (as
+ *      fa_bwd_qk_deterministic).
+ * Tq and Tk up to 2^28, (T / 128 + B + 1) Hq up to 2^29 (FA_ERR_UNSUPPORTED above). */
+size_t fa_fwd_packed_workspace_size(int B, int Tq, int Hq, int Hkv, int d);
+fa_status fa_fwd_packed(const fa_rows* Q, const fa_rows* K, const fa_rows* V, const int* cu_q,
+                        const int* cu_k, int B, int Tq, int Tk, int Hq, int Hkv, int d,
+                        int mask_kind, float scale, const fa_rows* O, float* LSE, void* workspace,
+                        size_t workspace_bytes, void* stream);
+size_t fa_bwd_packed_workspace_size(int B, int Tq, int Tk, int Hq, int Hkv, int d);
+fa_status fa_bwd_packed(const fa_rows* Q, const fa_rows* K, const fa_rows* V, const fa_rows* O,
+                        const fa_rows* dO, const float* LSE, const int* cu_q, const int* cu_k,
+                        int B, int Tq, int Tk, int Hq, int Hkv, int d, int mask_kind, float scale,
+                        int deterministic, const fa_rows* dQ, const fa_rows* dK, const fa_rows* dV,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- Paged key/value cache -------------------------------------------------
  * A pool of pages shared by the sequences of a batch.  Position p of sequence
  * b lies in slot p % page_size of page page_table[b][p / page_size]; the pools
@@ -229,14 +270,6 @@ typedef struct {
   int B, max_pages;
   int64_t table_stride;
 } fa_paged_cache;
-
-/* Rows [rows, heads, d] of bf16 (one row a token), d contiguous, 16-byte
- * aligned; strides in elements, multiples of 8: a slice of a fused projection
- * needs no copy. */
-typedef struct {
-  void* data;
-  int64_t row_stride, head_stride;
-} fa_rows;
 
 /* Write new keys and values into the cache.
  * In:  K, V: T rows of Hkv heads; row t belongs to the sequence b with
