@@ -708,7 +708,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = issue_dp(qd_iter);
           if (!ok) break;
         }
-        for (int n = 0; ok && more<MODE>(p, it, i); ++n) {
+        int n = 0;  // query tiles done
+        for (; ok && more<MODE>(p, it, i); ++n) {
           const Step inext = next_step<MODE>(p, it, i);
           const bool again = more<MODE>(p, it, inext);
           const uint32_t st = qd_iter % C::NST;         // stage of query tile i
@@ -763,7 +764,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           i = inext;
         }
         if (!ok) break;
-        tc_commit(&dkdv_full);
+        // Only an item with a query tile has gradients to hand over.  (Its
+        // softmax has then read the item before; after an item without one
+        // this thread could otherwise complete the barrier twice while the
+        // softmax still waits for the first time, which it would then miss.)
+        if (n > 0) tc_commit(&dkdv_full);
         tc_commit(&kv_empty);
       }
       if (issued) {
@@ -899,9 +904,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
       // ---- epilogue: dV and dK rows of this key tile
-      ok = mbar_wait_warp(&dkdv_full, dk_cnt & 1, w);
-      if (!ok) break;
-      ++dk_cnt;
+      if (any) {  // without a query tile the rows are zeros, and nothing is handed over
+        ok = mbar_wait_warp(&dkdv_full, dk_cnt & 1, w);
+        if (!ok) break;
+        ++dk_cnt;
+      }
       tc_fence_after();
       const int prow = MODE == PACKED ? key - pack::pad(it.Lk) : key;  // PACKED: row of the sequence
       const bool store = MODE == PACKED ? prow >= 0 : key < p.Nk;

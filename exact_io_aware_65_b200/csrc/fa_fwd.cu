@@ -506,7 +506,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           jn = jnn;
         }
         if (!ok) break;
-        for (int t = t_lo; t < t_hi && t < tiles; ++t) tc_commit(&o_full[t]);
+        // (A tile without a key has no O to hand over: were its barrier completed
+        // all the same, two such items in a row could complete it twice while
+        // the softmax still waits for the first time.)
+        for (int t = t_lo; t < t_hi && t < tiles; ++t)
+          if (!first_pv[t]) tc_commit(&o_full[t]);
         if (!q_released) tc_commit(&q_empty[0]);
       }
       }
@@ -701,7 +705,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // the tile's last PV (none if no key tile reached the tile: then
         // l = 0 and O is written as zeros)
         if (!first) ok = mbar_wait_warp(&pv_done[t], (np - 1) & 1, w);
-      } else {
+      } else if (!first) {
         ok = mbar_wait_warp(&o_full[t], o_cnt & 1, w);
         ++o_cnt;
       }
