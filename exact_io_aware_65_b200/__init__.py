@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -70,6 +71,12 @@ SIGNATURES = {
 }
 
 
+# The structures of include/fa.h.  The calls below pass them as packed bytes (the
+# same layout): filling a ctypes structure field by field takes longer than the
+# smallest kernels.
+_ROWS, _CACHE = struct.Struct("@Pqq"), struct.Struct("@PPiiiiiqqqPPPiiq")
+
+
 class _Rows(ctypes.Structure):
     """fa_rows of include/fa.h."""
     _fields_ = [("data", _vp), ("row_stride", _i64), ("head_stride", _i64)]
@@ -80,6 +87,14 @@ class _PagedCache(ctypes.Structure):
     _fields_ = [("K", _vp), ("V", _vp), ("dtype", _i), ("num_pages", _i), ("page_size", _i), ("Hkv", _i), ("d", _i),
                 ("page_stride", _i64), ("head_stride", _i64), ("row_stride", _i64), ("k_scale", _vp),
                 ("v_scale", _vp), ("page_table", _vp), ("B", _i), ("max_pages", _i), ("table_stride", _i64)]
+
+
+class _Cache:
+    """A checked cache: its packed fa_paged_cache, and the sizes that the calls go by."""
+    __slots__ = ("c", "B", "Hkv", "d", "max_pages", "page_size")
+
+    def __init__(self, c, B, Hkv, d, max_pages, page_size):
+        self.c, self.B, self.Hkv, self.d, self.max_pages, self.page_size = c, B, Hkv, d, max_pages, page_size
 
 
 class FAError(RuntimeError):
@@ -113,8 +128,8 @@ def _check(code: int, what: str):
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current device's current stream, without building a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -335,10 +350,13 @@ def decode(Q, K, V, mask="none", scale=None, O=None, LSE=None, workspace=None, s
 def _run(name, device, stream, *args):
     """Call ``name`` with ``device`` current (its kernels launch there) on
     ``stream``, by default that device's current stream."""
-    if device.index != torch.cuda.current_device():
+    if device.index != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
-            return _check(getattr(lib(), name)(*args, _stream(stream)), name)
-    _check(getattr(lib(), name)(*args, _stream(stream)), name)
+            code = getattr(lib(), name)(*args, _stream(stream))
+    else:
+        code = getattr(_lib or lib(), name)(*args, _stream(stream))
+    if code:
+        raise FAError(code, name)
 
 
 def _empty(shape, dtype, device, stream):
@@ -352,10 +370,13 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+_BF16, _E4M3 = torch.bfloat16, torch.float8_e4m3fn
+
+
 def _rows(t, name, heads=None, d=None, rows=None, device=None):
     """fa_rows of a bf16 CUDA tensor [rows, heads, d] whose last dimension is
     contiguous; the rows and heads may be strided."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 3):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is _BF16 and t.dim() == 3):
         raise FAError(1, f"{name} must be a bf16 CUDA tensor [rows, heads, d]")
     n, h, w = t.shape
     if (heads is not None and h != heads) or (d is not None and w != d) or (rows is not None and n != rows):
@@ -364,11 +385,15 @@ def _rows(t, name, heads=None, d=None, rows=None, device=None):
     if device is not None and t.device != device:
         raise FAError(1, f"{name} must be on {device}, got {t.device}")
     rs, hs, ds = t.stride()
-    rs, hs = rs if n > 1 else h * w, hs if h > 1 else w  # the stride of a single row or head is never used
-    if (ds != 1 and w > 1) or rs % 8 or hs % 8 or t.data_ptr() % 16:
+    if n <= 1:  # the stride of a single row or head is never used
+        rs = h * w
+    if h <= 1:
+        hs = w
+    ptr = t.data_ptr()
+    if (ds != 1 and w > 1) or (rs | hs) & 7 or ptr & 15:
         raise FAError(1, f"{name}: d must be contiguous, and rows and heads start on 16-byte boundaries (strides "
                          f"{t.stride()})")
-    return _Rows(t.data_ptr(), rs, hs)
+    return _ROWS.pack(ptr, rs, hs)
 
 
 def _int32(t, name, n, device):
@@ -429,9 +454,9 @@ def fwd_packed(Q, K, V, cu_q, cu_k, mask="none", scale=None, O=None, LSE=None, w
     if workspace is None and need:
         workspace = _empty(need, torch.uint8, dev, stream)
     wp, wn = (None, 0) if workspace is None else _workspace(workspace, need, dev)
-    _run("fa_fwd_packed", dev, stream, ctypes.byref(q), ctypes.byref(k), ctypes.byref(v),
+    _run("fa_fwd_packed", dev, stream, q, k, v,
          _int32(cu_q, "cu_q", B + 1, dev), _int32(cu_k, "cu_k", B + 1, dev), B, Tq, Tk, Hq, Hkv, d, _packed_mask(mask),
-         scale, ctypes.byref(o), LSE.data_ptr(), wp, wn)
+         scale, o, LSE.data_ptr(), wp, wn)
     return O, LSE
 
 
@@ -461,39 +486,39 @@ def bwd_packed(Q, K, V, O, dO, LSE, cu_q, cu_k, mask="none", scale=None, dQ=None
     if workspace is None:
         workspace = _empty(need, torch.uint8, dev, stream)
     wp, wn = _workspace(workspace, need, dev)
-    _run("fa_bwd_packed", dev, stream, ctypes.byref(q), ctypes.byref(k), ctypes.byref(v), ctypes.byref(o), ctypes.byref(g),
+    _run("fa_bwd_packed", dev, stream, q, k, v, o, g,
          LSE.data_ptr(), _int32(cu_q, "cu_q", B + 1, dev), _int32(cu_k, "cu_k", B + 1, dev), B, Tq, Tk, Hq, Hkv, d,
-         _packed_mask(mask), scale, 1 if deterministic else 0, ctypes.byref(dq), ctypes.byref(dk), ctypes.byref(dv), wp, wn)
+         _packed_mask(mask), scale, 1 if deterministic else 0, dq, dk, dv, wp, wn)
     return dQ, dK, dV
 
 
 def _paged_cache(k_cache, v_cache, page_table, k_scale=None, v_scale=None, scales=True):
     """fa_paged_cache of two pools [pages, Hkv, page_size, d]."""
     for t in (k_cache, v_cache):
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4
-                and t.dtype in (torch.bfloat16, torch.float8_e4m3fn)):
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4 and (t.dtype is _BF16 or t.dtype is _E4M3)):
             raise FAError(1, "cache pools must be bf16 or float8_e4m3fn CUDA tensors [pages, Hkv, page_size, d]")
     dev = k_cache.device
-    if (k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or v_cache.device != dev
-            or k_cache.stride() != v_cache.stride()):
-        raise FAError(1, "the K and V pools must have one shape, type, device and layout")
     pages, Hkv, page, d = k_cache.shape
-    eight = k_cache.dtype == torch.float8_e4m3fn
-    unit = 16 if eight else 8
-    sp, sh, sr, sd = k_cache.stride()
+    sp, sh, sr, sd = strides = k_cache.stride()
+    if (v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype or v_cache.device != dev
+            or v_cache.stride() != strides):
+        raise FAError(1, "the K and V pools must have one shape, type, device and layout")
+    eight = k_cache.dtype is _E4M3
     # (the stride of a dimension of one entry is never used)
     sp, sh, sr = sp if pages > 1 else 0, sh if Hkv > 1 else 0, sr if page > 1 else 0
-    if (sd != 1 and d > 1) or sp % unit or sh % unit or sr % unit or k_cache.data_ptr() % 16 or v_cache.data_ptr() % 16:
+    kp, vp = k_cache.data_ptr(), v_cache.data_ptr()
+    if (sd != 1 and d > 1) or (sp | sh | sr) & (15 if eight else 7) or (kp | vp) & 15:
         raise FAError(1, "cache rows must be contiguous and start on 16-byte boundaries")
-    ks = vs = None
+    ks = vs = 0
     if eight and scales:
         ks = _check_buf(k_scale, "k_scale", (Hkv,), torch.float32, dev).data_ptr()
         vs = _check_buf(v_scale, "v_scale", (Hkv,), torch.float32, dev).data_ptr()
     elif k_scale is not None or v_scale is not None:
         raise FAError(1, "k_scale and v_scale belong to float8_e4m3fn pools")
     tp, width, ts = _table(page_table, "page_table", dev)
-    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), 1 if eight else 0, pages, page, Hkv, d, sp, sh, sr, ks,
-                       vs, tp, page_table.shape[0], width, ts)
+    B = page_table.shape[0]
+    return _Cache(_CACHE.pack(kp, vp, 1 if eight else 0, pages, page, Hkv, d, sp, sh, sr, ks, vs, tp, B, width, ts), B,
+                  Hkv, d, width, page)
 
 
 def _weights(t, name, B, Hkv, least, device):
@@ -515,7 +540,7 @@ def paged_append(K, V, cu_seqlens, lens, k_cache, v_cache, page_table, k_scale=N
     dev = k_cache.device
     k = _rows(K, "K", c.Hkv, c.d, device=dev)
     v = _rows(V, "V", c.Hkv, c.d, K.shape[0], dev)
-    _run("fa_paged_append", dev, stream, ctypes.byref(c), ctypes.byref(k), ctypes.byref(v),
+    _run("fa_paged_append", dev, stream, c.c, k, v,
          _int32(cu_seqlens, "cu_seqlens", c.B + 1, dev), _int32(lens, "lens", c.B, dev), K.shape[0])
 
 
@@ -551,7 +576,7 @@ def paged_decode(Q, k_cache, v_cache, page_table, lens, scale=None, k_scale=None
     if workspace is None:
         workspace = _empty(need, torch.uint8, dev, stream)
     sp, sn = _workspace(workspace, need, dev)
-    _run("fa_paged_decode", dev, stream, ctypes.byref(c), ctypes.byref(q), Hq, lp, scale, wp or None, wb, wh,
+    _run("fa_paged_decode", dev, stream, c.c, q, Hq, lp, scale, wp or None, wb, wh,
          1 if accumulate else 0, O.data_ptr(), LSE.data_ptr(), sp, sn)
     return O, LSE
 
@@ -580,7 +605,7 @@ def paged_evict(weights, k_cache, v_cache, page_table, lens, table_out, budget, 
         _check_buf(kept, "kept", (B, Hkv, budget), torch.int32, dev)
     lens_out = _empty((B,), torch.int32, dev, stream) if lens_out is None else \
         _check_buf(lens_out, "lens_out", (B,), torch.int32, dev)
-    _run("fa_paged_evict", dev, stream, ctypes.byref(c), lp, tp, ts, width, wp, wb, wh, budget, recent, op, ob, oh,
+    _run("fa_paged_evict", dev, stream, c.c, lp, tp, ts, width, wp, wb, wh, budget, recent, op, ob, oh,
          weights_out.shape[2], kept.data_ptr(), lens_out.data_ptr())
     return kept, lens_out
 

@@ -33,6 +33,15 @@ uint32_t* status_word() {
 static std::atomic<uint64_t> g_wait_timeout_ns{4000000000ull};
 uint64_t wait_timeout_ns() { return g_wait_timeout_ns.load(); }
 
+bool allow_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (done.load(std::memory_order_relaxed) >> dev & 1) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return true;
+}
+
 int num_sms() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;

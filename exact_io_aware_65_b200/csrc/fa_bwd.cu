@@ -205,6 +205,8 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const PackedArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane / LPR, li = lane % LPR;
   const int slot = blockIdx.x / a.pk.Hq, h = blockIdx.x % a.pk.Hq;
+  pdl_wait();
+  pdl_next();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.sched = 0u;
   const int b = pack::sequence_of_slot(a.pk, slot);
   if (b < 0) return;
@@ -252,6 +254,8 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const PackedArgs a) {
 template <int D>
 __global__ void __launch_bounds__(256) packed_convert_kernel(const PackedArgs a, unsigned dq_blocks) {
   constexpr int G = 4;  // four 4-column groups a thread, as dq_convert_kernel
+  pdl_wait();
+  pdl_next();
   if (blockIdx.x < dq_blocks) {
     const int slot = blockIdx.x / a.pk.Hq, h = blockIdx.x % a.pk.Hq;
     const int b = pack::sequence_of_slot(a.pk, slot);
@@ -484,6 +488,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (MODE == PACKED) {
+    pdl_wait();
+    pdl_next();
+  }
   const uint32_t tmem = tmem_base_sh;
   const WaitCtx w{p.timeout_ns, &abort_flag, p.status};
 
@@ -819,7 +827,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int kq = no_key ? INT_MAX : (cmask ? (MODE == PACKED ? kr - hf * 64 : key - (i * BQ + hf * 64 + it.off)) : INT_MIN);
         // ---- P^T = exp2(S^T * scale * log2e - LSE_i * log2e), kept packed
         // as bf16 pairs (the form the dV product reads) for the dS step too.
+        // (PACKED: the dS step takes P as it was before that rounding -- it is
+        // in registers all the same, and dQ and dK then carry one rounding to
+        // bf16 instead of two.)
         uint32_t pk[32];
+        float pf[MODE == PACKED ? 64 : 1];
         {
           uint32_t sr[64];
           FA_TMEM_LD_X32(tmem + lane_bits + C::COL_S + hf * 64, sr);
@@ -844,6 +856,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             pk[2 * u] = pack_bf16x2(pv[0], pv[1]);
             pk[2 * u + 1] = pack_bf16x2(pv[2], pv[3]);
+            if constexpr (MODE == PACKED) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) pf[4 * u + e] = pv[e];
+            }
           }
         }
         // over the first 32 of this half's own 64 score columns, all loaded
@@ -870,8 +886,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                          make_float2(dv.x, dv.y));
             const float2 t1 = __fadd2_rn(make_float2(__uint_as_float(dr[u * 4 + 2]), __uint_as_float(dr[u * 4 + 3])),
                                          make_float2(dv.z, dv.w));
-            const float2 g01 = __fmul2_rn(make_float2(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u)), t0);
-            const float2 g23 = __fmul2_rn(make_float2(__uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u)), t1);
+            float2 p01 = make_float2(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u));
+            float2 p23 = make_float2(__uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u));
+            if constexpr (MODE == PACKED) {
+              p01 = make_float2(pf[cc * 32 + 4 * u], pf[cc * 32 + 4 * u + 1]);
+              p23 = make_float2(pf[cc * 32 + 4 * u + 2], pf[cc * 32 + 4 * u + 3]);
+            }
+            const float2 g01 = __fmul2_rn(p01, t0);
+            const float2 g23 = __fmul2_rn(p23, t1);
             dk[cc * 16 + u * 2 + 0] = pack_bf16x2(g01.x, g01.y);
             dk[cc * 16 + u * 2 + 1] = pack_bf16x2(g23.x, g23.y);
           }
@@ -1317,8 +1339,7 @@ static fa_status launch_bwd_packed_d(const PackedProblem& pr, const CUtensorMap&
   a.scale = pr.scale;
   a.status = st;
   const unsigned blocks = (unsigned)(pack::slots(k.Tq, k.B) * k.Hq);
-  bwd::packed_prep_kernel<D><<<blocks, 256, 0, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (!launch_early(bwd::packed_prep_kernel<D>, blocks, 256, 0, s, a)) return FA_ERR_CUDA;
   if (k.Tk > 0) {
     bwd::Params p = {};
     p.pk = k;
@@ -1347,16 +1368,19 @@ static fa_status launch_bwd_packed_d(const PackedProblem& pr, const CUtensorMap&
     p.status = st;
     constexpr int smem = bwd::Cfg<D>::SMEM_BYTES;
     auto kern = bwd::main_kernel<D, PACKED>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FA_ERR_CUDA;
+    static std::atomic<uint64_t> done{0};
     const int sms = num_sms();
-    kern<<<p.n_items < sms ? p.n_items : sms, bwd::NUM_THREADS, smem, s>>>(mQ, mK, mV, mdO, mdK, mdV, p);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (!allow_smem(done, (const void*)kern, smem) ||
+        !launch_early(kern, (unsigned)(p.n_items < sms ? p.n_items : sms), bwd::NUM_THREADS, smem, s, mQ, mK, mV, mdO, mdK,
+                      mdV, p))
+      return FA_ERR_CUDA;
   }
   const long long add = part ? ((long long)2 * k.Tk * k.Hkv * (D / 8) + 255) / 256 : 0;
   const unsigned dq_blocks = k.Tq > 0 ? blocks : 0;
   const unsigned more = (unsigned)(add < (1 << 20) ? add : (1 << 20));
-  if (dq_blocks + more > 0) bwd::packed_convert_kernel<D><<<dq_blocks + more, 256, 0, s>>>(a, dq_blocks);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  if (dq_blocks + more > 0 && !launch_early(bwd::packed_convert_kernel<D>, dq_blocks + more, 256, 0, s, a, dq_blocks))
+    return FA_ERR_CUDA;
+  return FA_OK;
 }
 
 fa_status launch_bwd_packed(const PackedProblem& pr, const Rows& Q, const Rows& K, const Rows& V, const Rows& O,

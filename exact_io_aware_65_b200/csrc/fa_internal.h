@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "fa.h"
 #include "pack.cuh"
 
@@ -57,6 +59,27 @@ bool make_map_packed(CUtensorMap* map, const Rows& r, int T, int heads, int d);
 
 // Same for a 2-D row-major bf16 matrix [rows, cols] (used by the self-test).
 bool make_map_bf16_2d(CUtensorMap* map, const void* base, int rows, int cols, int box_rows);
+
+// Sets a kernel's dynamic shared memory limit, once per device and kernel
+// (`done` is the kernel's own, one bit per device).
+bool allow_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes);
+
+// Launches a kernel that may be set up while the kernel before it in the stream
+// still runs: it calls pdl_wait() before it reads or writes anything.
+template <typename... P, typename... A>
+inline bool launch_early(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess;
+}
 
 uint64_t wait_timeout_ns();
 // Device address of the calling device's status word (nullptr on failure).

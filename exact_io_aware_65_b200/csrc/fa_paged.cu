@@ -59,6 +59,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // A warp per (token, K or V): 16 bytes of the input a lane.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendParams p) {
+  pdl_wait();
+  pdl_next();
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * (APPEND_THREADS / 32) + (threadIdx.x >> 5);
   const int t = (int)(unit >> 1), kv = (int)(unit & 1);
@@ -137,6 +139,8 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParam
   __shared__ int above_w[32], tie_w[32];
   __shared__ uint32_t sh_prefix;
   __shared__ int sh_need;
+  pdl_wait();
+  pdl_next();
   const int bh = blockIdx.x, b = bh / p.Hkv, h = bh % p.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = clamp_len(p.c, __ldg(p.lens + b));
@@ -242,6 +246,8 @@ constexpr int MOVE_ROWS = 4;
 
 template <int ROWB>
 __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const EvictParams p) {
+  pdl_wait();
+  pdl_next();
   constexpr int LPR = ROWB / 16, GROUPS = MOVE_THREADS / LPR, PER = GROUPS * MOVE_ROWS;
   const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const int b = bh / p.Hkv, h = bh % p.Hkv;
@@ -310,13 +316,9 @@ fa_status launch_paged_append(const PagedCache& c, const Rows& K, const Rows& V,
   constexpr int WARPS = paged::APPEND_THREADS / 32;
   const unsigned grid = (unsigned)((2LL * T + WARPS - 1) / WARPS);
   const bool e4m3 = c.elem == 1;
-  if (c.d == 64)
-    e4m3 ? paged::append_kernel<64, true><<<grid, paged::APPEND_THREADS, 0, s>>>(p)
-         : paged::append_kernel<64, false><<<grid, paged::APPEND_THREADS, 0, s>>>(p);
-  else
-    e4m3 ? paged::append_kernel<128, true><<<grid, paged::APPEND_THREADS, 0, s>>>(p)
-         : paged::append_kernel<128, false><<<grid, paged::APPEND_THREADS, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  auto* kern = c.d == 64 ? (e4m3 ? paged::append_kernel<64, true> : paged::append_kernel<64, false>)
+                         : (e4m3 ? paged::append_kernel<128, true> : paged::append_kernel<128, false>);
+  return launch_early(kern, grid, paged::APPEND_THREADS, 0, s, p) ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status launch_paged_evict(const PagedCache& c, const Evict& e, cudaStream_t s) {
@@ -345,21 +347,21 @@ fa_status launch_paged_evict(const PagedCache& c, const Evict& e, cudaStream_t s
   // shared memory for the keys a head can have to choose from, when they fit
   const long long most = (long long)c.max_pages * c.page_size - e.recent;
   const int smem = 4 * (int)(most < 0 ? 0 : most < paged::SEL_SMEM_KEYS ? most : paged::SEL_SMEM_KEYS);
-  if (cudaFuncSetAttribute(paged::select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           4 * paged::SEL_SMEM_KEYS) != cudaSuccess)
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(done, (const void*)paged::select_kernel, 4 * paged::SEL_SMEM_KEYS) ||
+      !launch_early(paged::select_kernel, (unsigned)(c.B * c.Hkv), paged::SEL_THREADS, smem, s, p))
     return FA_ERR_CUDA;
-  paged::select_kernel<<<c.B * c.Hkv, paged::SEL_THREADS, smem, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  bool ok;
   auto move = [&](auto kern, int rowb) {
     const int per = paged::MOVE_THREADS / (rowb / 16) * paged::MOVE_ROWS;
     p.chunks = (e.budget + per - 1) / per;
-    kern<<<c.B * c.Hkv * p.chunks, paged::MOVE_THREADS, 0, s>>>(p);
+    ok = launch_early(kern, (unsigned)(c.B * c.Hkv * p.chunks), paged::MOVE_THREADS, 0, s, p);
   };
   const int rowb = c.d * c.elem;
   if (rowb == 64) move(paged::move_kernel<64>, 64);
   else if (rowb == 128) move(paged::move_kernel<128>, 128);
   else move(paged::move_kernel<256>, 256);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return ok ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace fa

@@ -125,6 +125,8 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
   __shared__ int start_b;
   __shared__ long long sh_total;
 
+  pdl_wait();
+  pdl_next();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int HU = p.Hkv * p.HB, cta = blockIdx.x;
@@ -469,8 +471,10 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
 
 // Block (c, r): row r of the unit that begins in CTA c and ends in another.
 template <int D>
-__global__ void __launch_bounds__(D) join_kernel(const DecodeParams p) {
-  const int c0 = blockIdx.x, r = blockIdx.y, col = threadIdx.x;
+__global__ void __launch_bounds__(D) join_kernel(const DecodeParams p, int rows) {
+  pdl_wait();
+  pdl_next();
+  const int c0 = blockIdx.x / rows, r = blockIdx.x % rows, col = threadIdx.x;
   const int4 u = p.desc[c0];
   if (u.x < 0) return;
   const int hk = u.y / p.HB, row0 = (u.y % p.HB) * ROWS;
@@ -498,6 +502,8 @@ __global__ void __launch_bounds__(D) join_kernel(const DecodeParams p) {
 constexpr int W_THREADS = 256;
 __global__ void __launch_bounds__(W_THREADS) weights_kernel(const DecodeParams p, float* A, long long a_batch,
                                                             long long a_head, int accumulate, int chunks) {
+  pdl_wait();
+  pdl_next();
   const int bh = blockIdx.x / chunks, b = bh / p.Hkv, hk = bh % p.Hkv;
   const int len = clamp_len(p.c, __ldg(p.lens + b));
   const long long first = (long long)b * p.Hq + hk * p.G;
@@ -540,8 +546,8 @@ static fa_status launch_d(paged::DecodeParams p, int B, const PagedDecode& a, in
   constexpr int NST = RING_BYTES / STAGE < 6 ? RING_BYTES / STAGE : 6;
   constexpr int smem = WARPS * NST * STAGE + WARPS / 2 * ROWS * D * 4;
   static_assert(smem + 2048 <= 227 * 1024 && WARPS / 2 * ROWS * D * 4 >= MAX_BATCH * 4, "shared memory");
-  if (cudaFuncSetAttribute(partial_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return FA_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(done, (const void*)partial_kernel<D, E4M3>, smem)) return FA_ERR_CUDA;
   const int* lens = p.lens;
   const int* table = p.c.table;
   const __nv_bfloat16* Q = p.Q;
@@ -556,16 +562,15 @@ static fa_status launch_d(paged::DecodeParams p, int B, const PagedDecode& a, in
     p.O = O + (long long)b0 * p.Hq * D;
     p.LSE = LSE + (long long)b0 * p.Hq;
     if (scores) p.scores = scores + (long long)b0 * p.Hq * p.pitch;
-    partial_kernel<D, E4M3><<<grid, THREADS, smem, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-    join_kernel<D><<<dim3(grid, p.G < ROWS ? p.G : ROWS), D, 0, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (!launch_early(partial_kernel<D, E4M3>, (unsigned)grid, THREADS, smem, s, p)) return FA_ERR_CUDA;
+    const int rows = p.G < ROWS ? p.G : ROWS;
+    if (!launch_early(join_kernel<D>, (unsigned)(grid * rows), D, 0, s, p, rows)) return FA_ERR_CUDA;
     if (scores) {
       long long chunks = (p.pitch + 4 * W_THREADS - 1) / (4 * W_THREADS);
       if (chunks > 64) chunks = 64;
-      weights_kernel<<<(unsigned)(p.B * p.Hkv * chunks), W_THREADS, 0, s>>>(
-          p, a.W + b0 * a.w_batch, a.w_batch, a.w_head, a.accumulate, (int)chunks);
-      if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+      if (!launch_early(weights_kernel, (unsigned)(p.B * p.Hkv * chunks), W_THREADS, 0, s, p, a.W + b0 * a.w_batch,
+                        a.w_batch, a.w_head, a.accumulate, (int)chunks))
+        return FA_ERR_CUDA;
     }
   }
   return FA_OK;

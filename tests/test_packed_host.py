@@ -113,6 +113,13 @@ def test_the_backward_refuses_more():
         assert calls(over)[1] == code, over
 
 
+def test_the_binding_packs_the_header_s_structures():
+    for packed, struct in ((fa._ROWS, fa._Rows), (fa._CACHE, fa._PagedCache)):
+        n = len(struct._fields_)
+        assert packed.size == ctypes.sizeof(struct)
+        assert packed.pack(*range(1, n + 1)) == bytes(struct(*range(1, n + 1)))
+
+
 def test_nothing_to_do():
     empty = dict(Tq=0, Q=rows(data=0), O=rows(data=0), dO=rows(data=0), dQ=rows(data=0))
     assert calls(empty | dict(Tk=0, K=rows(data=0), V=rows(data=0), dK=rows(data=0), dV=rows(data=0), ws=None)) == (0, 0)
