@@ -204,9 +204,8 @@ template <int D>
 __global__ void __launch_bounds__(256) packed_prep_kernel(const PackedArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane / LPR, li = lane % LPR;
-  const int slot = blockIdx.x / a.pk.Hq, h = blockIdx.x % a.pk.Hq;
   pdl_wait();
-  pdl_next();
+  const int slot = blockIdx.x / a.pk.Hq, h = blockIdx.x % a.pk.Hq;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.sched = 0u;
   const int b = pack::sequence_of_slot(a.pk, slot);
   if (b < 0) return;
@@ -215,8 +214,9 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const PackedArgs a) {
   if (i >= pack::tiles(s.Lq)) return;  // a slot that no tile uses
   if (threadIdx.x == 0) a.turn[blockIdx.x] = 0u;
   const int first = i * 128 - pack::pad(s.Lq);  // row of the sequence (negative: none)
-  for (int r = (threadIdx.x >> 5) * RPW + sub; r < 128; r += 8 * RPW) {
-    const int n = first + r;
+#pragma unroll
+  for (int k = 0; k < 128 / (8 * RPW); ++k) {  // all of a thread's loads in flight at once
+    const int r = (k * 8 + (threadIdx.x >> 5)) * RPW + sub, n = first + r;
     float acc = 0.0f;
     if (n >= 0 && FA_IN_BOUNDS(a.status, s.sq + n, 1, a.pk.Tq)) {
       const long long t = s.sq + n;
@@ -249,33 +249,33 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const PackedArgs a) {
   }
 }
 
-// dQ = bf16(scale * accumulator), a block per (slot, head); the blocks behind
-// these add up the parts of dK and dV, in order.
+// dQ = bf16(scale * accumulator): a block per (slot, head) and 32 columns; the
+// blocks behind these add up the parts of dK and dV, in order.
 template <int D>
 __global__ void __launch_bounds__(256) packed_convert_kernel(const PackedArgs a, unsigned dq_blocks) {
   constexpr int G = 4;  // four 4-column groups a thread, as dq_convert_kernel
-  pdl_wait();
-  pdl_next();
   if (blockIdx.x < dq_blocks) {
-    const int slot = blockIdx.x / a.pk.Hq, h = blockIdx.x % a.pk.Hq;
+    constexpr int QUARTERS = D / 32;
+    const int tile = blockIdx.x / QUARTERS;
+    const int slot = tile / a.pk.Hq, h = tile % a.pk.Hq;
     const int b = pack::sequence_of_slot(a.pk, slot);
     if (b < 0) return;
     const pack::Seq s = pack::seq_at(a.pk, b);
     const int i = slot - pack::slot_base(s.sq, b);
     if (i >= pack::tiles(s.Lq)) return;
     const int first = i * 128 - pack::pad(s.Lq);
-    const float4* t = reinterpret_cast<const float4*>(a.dq_acc + (size_t)blockIdx.x * 128 * D);
+    const float4* t = reinterpret_cast<const float4*>(a.dq_acc + (size_t)tile * 128 * D);
+    const int eb = (blockIdx.x % QUARTERS) * 2 + threadIdx.x / 128, r = threadIdx.x % 128, n = first + r;
+    if (n < 0 || !FA_IN_BOUNDS(a.status, s.sq + n, 1, a.pk.Tq)) return;
+    uint4* dst = reinterpret_cast<uint4*>(a.dQ + (long long)(s.sq + n) * a.dq_row + h * a.dq_head + 4 * G * eb);
+    float4 v[G];
 #pragma unroll
-    for (int k = threadIdx.x; k < 128 * (D / (4 * G)); k += 256) {
-      const int eb = k / 128, r = k % 128, n = first + r;
-      if (n < 0 || !FA_IN_BOUNDS(a.status, s.sq + n, 1, a.pk.Tq)) continue;
-      uint4* dst = reinterpret_cast<uint4*>(a.dQ + (long long)(s.sq + n) * a.dq_row + h * a.dq_head + 4 * G * eb);
+    for (int u = 0; u < G; ++u) v[u] = t[(eb * G + u) * 128 + r];
 #pragma unroll
-      for (int u = 0; u < G / 2; ++u) {
-        const float4 x = t[(eb * G + 2 * u) * 128 + r], y = t[(eb * G + 2 * u + 1) * 128 + r];
-        dst[u] = make_uint4(pack_bf16x2(x.x * a.scale, x.y * a.scale), pack_bf16x2(x.z * a.scale, x.w * a.scale),
-                            pack_bf16x2(y.x * a.scale, y.y * a.scale), pack_bf16x2(y.z * a.scale, y.w * a.scale));
-      }
+    for (int u = 0; u < G / 2; ++u) {
+      const float4 x = v[2 * u], y = v[2 * u + 1];
+      dst[u] = make_uint4(pack_bf16x2(x.x * a.scale, x.y * a.scale), pack_bf16x2(x.z * a.scale, x.w * a.scale),
+                          pack_bf16x2(y.x * a.scale, y.y * a.scale), pack_bf16x2(y.z * a.scale, y.w * a.scale));
     }
     return;
   }
@@ -488,10 +488,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (MODE == PACKED) {
-    pdl_wait();
-    pdl_next();
-  }
   const uint32_t tmem = tmem_base_sh;
   const WaitCtx w{p.timeout_ns, &abort_flag, p.status};
 
@@ -552,10 +548,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // One thread; PACKED: the warp looks the items up together, and lane 0
     // issues the copies.
     if (MODE == PACKED || lane == 0) {
+      // (the other lanes wait for lane 0 between items)
       const bool lead = MODE != PACKED || lane == 0;
-      auto await = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return MODE == PACKED ? mbar_wait_warp(bar, parity, w) : mbar_wait(bar, parity, w);
-      };
       auto load = [&](uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int c, int y, int start, int head) {
         if (MODE == PACKED) tma_load_4d(dst + c * C::CHUNK_BYTES, m, bar, c * 64, y, start, head);
         else tma_load_3d(dst + c * C::CHUNK_BYTES, m, bar, c * 64, y, head);
@@ -565,7 +559,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool ok = true, q_only = false;  // q_only: the last tile's dO load was never issued
       for (;; ++item_iter) {
         const uint32_t slot = item_iter % RING;
-        ok = await(&item_empty[slot], ((item_iter / RING) & 1) ^ 1);
+        if (lead) ok = mbar_wait(&item_empty[slot], ((item_iter / RING) & 1) ^ 1, w);
+        if (MODE == PACKED) ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         // CTA b starts on item b, then claims items gridDim.x, gridDim.x + 1, ...
         int idx = (int)blockIdx.x;
@@ -579,7 +574,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           int b;
           pack::Seq sq;
           pack::Place at;
-          if (idx < p.n_items && pack::locate(p.pk, walk, idx, [&](const pack::Seq& x) { return packed_units(p, x); },
+          if (idx < p.n_items && pack::locate(p.pk, walk, idx, p.n_items, [&](const pack::Seq& x) { return packed_units(p, x); },
                                               [](const pack::Seq& x) { return x.Lq; }, b, sq, at))
             it = packed_item(p, sq, b, at);
           else
@@ -596,53 +591,49 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           mbar_arrive(&item_full[slot]);
         }
         if (idx >= p.n_items) break;
-        ok = await(&kv_empty, (item_iter & 1) ^ 1);
-        if (!ok) break;
-        const int yq = MODE == PACKED ? -pack::pad(it.Lq) : 0, yk = MODE == PACKED ? -pack::pad(it.Lk) : 0;
-        if (lead) {
+        if (lead) ok = mbar_wait(&kv_empty, (item_iter & 1) ^ 1, w);
+        if (lead && ok) {
+          const int yq = MODE == PACKED ? -pack::pad(it.Lq) : 0, yk = MODE == PACKED ? -pack::pad(it.Lk) : 0;
           mbar_arrive_expect_tx(&kv_full, 2 * C::TILE_BYTES);
-          const int head = MODE == PACKED ? it.hk : it.bh;
+          const int hkv = MODE == PACKED ? it.hk : it.bh;
 #pragma unroll
           for (int c = 0; c < C::CHUNKS; ++c) {
-            load(sK, &mapK, &kv_full, c, yk + it.j * BK, it.sk, head);
-            load(sV, &mapV, &kv_full, c, yk + it.j * BK, it.sk, head);
+            load(sK, &mapK, &kv_full, c, yk + it.j * BK, it.sk, hkv);
+            load(sV, &mapV, &kv_full, c, yk + it.j * BK, it.sk, hkv);
           }
-        }
-        for (Step i = first_step<MODE>(p, it); more<MODE>(p, it, i); i = next_step<MODE>(p, it, i)) {
-          const uint32_t st = qd_iter % C::NST;
-          const uint32_t par = ((qd_iter / C::NST) & 1) ^ 1;
-          uint8_t* q = sQD + st * 2 * C::TILE_BYTES;
-          const size_t row0 = row_of(it, i);
-          uint8_t* ld = smem + C::OFF_LD + st * 1024;
-          const int head = MODE == PACKED ? it.hk * p.pk.G + i.g : it.bh;
-          ok = await(&q_empty[st], par);
-          if (!ok) break;
-          if (lead) {
+          for (Step i = first_step<MODE>(p, it); more<MODE>(p, it, i); i = next_step<MODE>(p, it, i)) {
+            const uint32_t st = qd_iter % C::NST;
+            const uint32_t par = ((qd_iter / C::NST) & 1) ^ 1;
+            uint8_t* q = sQD + st * 2 * C::TILE_BYTES;
+            const size_t row0 = row_of(it, i);
+            uint8_t* ld = smem + C::OFF_LD + st * 1024;
+            const int head = MODE == PACKED ? it.hk * p.pk.G + i.g : it.bh;
+            ok = mbar_wait(&q_empty[st], par, w);
+            if (!ok) break;
             mbar_arrive_expect_tx(&q_full[st], C::TILE_BYTES + 512);
 #pragma unroll
             for (int c = 0; c < C::CHUNKS; ++c) load(q, &mapQ, &q_full[st], c, yq + i.i * BQ, it.sq, head);
             // (a debug build that finds row0 out of range loads the first rows
             // instead, so the barrier still gets its bytes)
             bulk_load(ld, p.L2w + (FA_IN_BOUNDS(p.status, row0, 128, ws_rows) ? row0 : 0), 512, &q_full[st]);
-          }
-          ok = await(&do_empty[st], par);
-          if (!ok) {
-            ++qd_iter;
-            q_only = true;
-            break;
-          }
-          if (lead) {
+            ok = mbar_wait(&do_empty[st], par, w);
+            if (!ok) {
+              ++qd_iter;
+              q_only = true;
+              break;
+            }
             mbar_arrive_expect_tx(&do_full[st], C::TILE_BYTES + 512);
 #pragma unroll
             for (int c = 0; c < C::CHUNKS; ++c)
               load(q + C::TILE_BYTES, &mapdO, &do_full[st], c, yq + i.i * BQ, it.sq, head);
             bulk_load(ld + 512, p.Dw + (FA_IN_BOUNDS(p.status, row0, 128, ws_rows) ? row0 : 0), 512, &do_full[st]);
+            ++qd_iter;
           }
-          ++qd_iter;
         }
+        if (MODE == PACKED) ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
       }
-      if (!ok) {
+      if (!ok && lead) {
         const uint64_t dl = globaltimer_ns() + 100000000ull;
         const uint32_t n = qd_iter < (uint32_t)C::NST ? qd_iter : (uint32_t)C::NST;
         for (uint32_t k = 0; k < n; ++k) {
@@ -1293,15 +1284,18 @@ fa_status launch_bwd(const Problem& pr, const void* Q, const void* K, const void
   return launch_bwd_d<128>(pr, mQ, mK, mV, mdO, O, dO, LSE, dQ, dK, dV, workspace, s, st, stage);
 }
 
-// Parts that a key head's query heads are divided into: with fewer key tiles
-// than fill the GPU twice, more of them, so that grouped heads do not leave SMs
-// idle.  (Each part writes dK and dV in fp32, and the last kernel adds them.)
+// Parts that a key head's query heads are divided into, so that every SM gets
+// four items or more and the longest of them do not end last: a key head's items
+// are as many times longer as it has query heads.  Each part writes dK and dV in
+// fp32, and the last kernel adds them.
 static int packed_parts(const Pack& k) {
   const long long items = (long long)(k.Tk / 128 + (k.B + 1) / 2) * k.Hkv;
-  const long long want = 2LL * num_sms();
+  const long long want = 4LL * num_sms();
   if (k.G == 1 || items >= want || items == 0) return 1;
   const long long n = (want + items - 1) / items;
-  return (int)(n < k.G ? n : k.G);
+  if (n >= k.G) return k.G;
+  const int each = (int)((k.G + n - 1) / n);  // query heads of a part, at most
+  return (k.G + each - 1) / each;
 }
 
 struct PackedWorkspace {
@@ -1369,18 +1363,18 @@ static fa_status launch_bwd_packed_d(const PackedProblem& pr, const CUtensorMap&
     constexpr int smem = bwd::Cfg<D>::SMEM_BYTES;
     auto kern = bwd::main_kernel<D, PACKED>;
     static std::atomic<uint64_t> done{0};
+    if (!allow_smem(done, (const void*)kern, smem)) return FA_ERR_CUDA;
+    // (set up behind the kernel before, this one and the next were slower by 2%:
+    // 1423 against 1378 us for 6100 + 8192 tokens, 52 against 50 us for 3440)
     const int sms = num_sms();
-    if (!allow_smem(done, (const void*)kern, smem) ||
-        !launch_early(kern, (unsigned)(p.n_items < sms ? p.n_items : sms), bwd::NUM_THREADS, smem, s, mQ, mK, mV, mdO, mdK,
-                      mdV, p))
-      return FA_ERR_CUDA;
+    kern<<<p.n_items < sms ? p.n_items : sms, bwd::NUM_THREADS, smem, s>>>(mQ, mK, mV, mdO, mdK, mdV, p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   }
   const long long add = part ? ((long long)2 * k.Tk * k.Hkv * (D / 8) + 255) / 256 : 0;
-  const unsigned dq_blocks = k.Tq > 0 ? blocks : 0;
+  const unsigned dq_blocks = k.Tq > 0 ? blocks * (D / 32) : 0;
   const unsigned more = (unsigned)(add < (1 << 20) ? add : (1 << 20));
-  if (dq_blocks + more > 0 && !launch_early(bwd::packed_convert_kernel<D>, dq_blocks + more, 256, 0, s, a, dq_blocks))
-    return FA_ERR_CUDA;
-  return FA_OK;
+  if (dq_blocks + more > 0) bwd::packed_convert_kernel<D><<<dq_blocks + more, 256, 0, s>>>(a, dq_blocks);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status launch_bwd_packed(const PackedProblem& pr, const Rows& Q, const Rows& K, const Rows& V, const Rows& O,

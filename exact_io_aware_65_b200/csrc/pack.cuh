@@ -95,19 +95,20 @@ __host__ __device__ __forceinline__ Place place_of(const Units& u, int r) {
 // that the items claimed last are short ones.  Warp-collective; lane L keeps
 // the sequence of rank L.  Claims only grow, so the walk never turns back.
 struct Walker {
-  int chunk = -32;      // first sequence of the 32 at hand
-  long long base = 0;   // items before them
-  long long total = 0;  // items of theirs
-  int seq = -1;         // this lane's sequence,
-  int items = 0;        // its items,
-  long long upto = 0;   // and theirs of the ranks up to it
+  int chunk = -32;  // first sequence of the 32 at hand
+  int base = 0;     // items before them
+  int seq = -1;     // this lane's sequence,
+  int from = 0;     // the chunk's items of the ranks before it,
+  int upto = 0;     // and with its own (lane 31: all)
 };
 
-// UnitsOf: (Seq) -> Units.  weight: items of equal sequences' longest first.
+// UnitsOf: (Seq) -> Units; Weight: (Seq) -> the length they are ranked by; most:
+// the items that the launch's sizes allow (a cu that is not ascending could
+// describe more, which are not done).
 template <typename UnitsOf, typename Weight>
-__device__ __forceinline__ void next_chunk(const Pack& k, Walker& w, UnitsOf units_of, Weight weight) {
+__device__ __forceinline__ void next_chunk(const Pack& k, Walker& w, int most, UnitsOf units_of, Weight weight) {
   const int lane = threadIdx.x & 31;
-  w.base += w.total;
+  w.base += __shfl_sync(0xffffffffu, w.upto, 31);
   w.chunk += 32;
   const int b = w.chunk + lane;
   int items = 0, wt = -1;
@@ -124,35 +125,36 @@ __device__ __forceinline__ void next_chunk(const Pack& k, Walker& w, UnitsOf uni
     rank += o > wt || (o == wt && i < lane);
   }
   w.seq = -1;
-  w.items = 0;
+  int mine = 0;
   for (int i = 0; i < n; ++i) {
     const int r = __shfl_sync(0xffffffffu, rank, i), x = __shfl_sync(0xffffffffu, items, i);
     if (r == lane) {
       w.seq = w.chunk + i;
-      w.items = x;
+      mine = x;
     }
   }
-  w.upto = w.items;
+  long long sum = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, w.upto, o);
-    if (lane >= o) w.upto += y;
+    const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += y;
   }
-  w.total = __shfl_sync(0xffffffffu, w.upto, 31);
+  w.upto = (int)min(sum, (long long)(most - w.base));
+  w.from = (int)min(sum - mine, (long long)(most - w.base));
 }
 
 // The sequence and place of item idx; false past the last.
 template <typename UnitsOf, typename Weight>
-__device__ __forceinline__ bool locate(const Pack& k, Walker& w, int idx, UnitsOf units_of, Weight weight, int& b,
+__device__ __forceinline__ bool locate(const Pack& k, Walker& w, int idx, int most, UnitsOf units_of, Weight weight, int& b,
                                        Seq& s, Place& at) {
-  while (idx >= w.base + w.total) {
+  while (idx - w.base >= __shfl_sync(0xffffffffu, w.upto, 31)) {
     if (w.chunk + 32 >= k.B) return false;
-    next_chunk(k, w, units_of, weight);
+    next_chunk(k, w, most, units_of, weight);
   }
-  const long long r = idx - w.base;
+  const int r = idx - w.base;
   const int src = __ffs(__ballot_sync(0xffffffffu, r < w.upto)) - 1;
   b = __shfl_sync(0xffffffffu, w.seq, src);
-  const int in = (int)(r - __shfl_sync(0xffffffffu, w.upto - w.items, src));
+  const int in = r - __shfl_sync(0xffffffffu, w.from, src);
   s = seq_at(k, b);
   at = place_of(units_of(s), in);
   return true;
