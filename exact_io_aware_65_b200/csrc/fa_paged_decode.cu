@@ -12,14 +12,20 @@
 // 128-key blocks of the batch, in order, whatever sequences they belong to
 // (paged.cuh).  A warp takes 16 keys of each block: it copies their rows into
 // its own ring in shared memory (cp.async, 16 bytes a lane, the row's place
-// looked up in the page table two steps ahead), and no warp waits for
-// another until the unit ends.  The G <= 16 query heads are the rows of
-// m16n8k16 matrix products: on the CUDA cores G multiply-adds a cache element
-// would take longer than the element's read from G = 8 on, and the 128-row
-// tiles of the tensor-memory products would be an eighth full.  The products
-// take their B operand with ldmatrix; 8-bit rows are widened to fp16 in
-// registers (exact), the queries are then scaled by a power of two into fp16's
-// range, and P is rounded to fp16 (2^-12 relative) rather than bf16.
+// looked up in the page table a step before), and no warp waits for another
+// until the unit ends.  Keys are the rows of both matrix products (m16n8k16),
+// S^T = K Q^T and O^T = V^T P^T, and the query heads the eight columns: G <= 8
+// heads fill half as much of the products as they would as rows, O takes half
+// the registers, and the maxima and sums of a head stay in its lanes.  (On the
+// CUDA cores G multiply-adds a cache element would take longer than the
+// element's read from G = 8 on; the 128-row tiles of the tensor-memory products
+// would be mostly empty.)  8-bit rows are widened to fp16 in registers (exact),
+// the queries are then scaled by a power of two into fp16's range, and P is
+// rounded to fp16 (2^-12 relative) rather than bf16.
+// The running maximum is lazy: a head takes it from its first keys and moves it
+// only when a score lies more than 8 (in log2 units) above it, so that a step
+// usually has no reduction over lanes; O / l does not depend on it, and 2^8
+// leaves fp16 room.
 // At the end of a unit the eight warps join their (O, m, l) in shared memory;
 // a unit that lies in one CTA is finished there, a part of one goes to the
 // workspace.
@@ -30,6 +36,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "fa_internal.h"
 #include "sm100.cuh"
 #include "paged.cuh"
@@ -37,9 +45,9 @@
 namespace fa {
 namespace paged {
 
-constexpr int ROWS = 16;  // query heads of a unit
+constexpr int ROWS = 16;  // query heads of a unit, at most: 8 in a tile, NB tiles
 constexpr int THREADS = WARPS * 32;
-constexpr int RING_BYTES = 192 * 1024 / WARPS;  // of each warp
+constexpr float SLACK = 8.0f;  // log2 units a score may lie above the reference maximum
 constexpr int MAX_BATCH = 4096;                 // sequences per launch (prefix of their blocks in shared memory)
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float LOG2E = 1.4426950408889634074f;
@@ -49,7 +57,10 @@ struct DecodeParams {
   const __nv_bfloat16* Q;
   long long q_row, q_head;  // elements
   const int* lens;
-  int B, Hq, Hkv, G, HB;    // HB: 16-head units of a key head's group
+  int B, Hq, Hkv, G, HB;    // HB: units of a key head's group
+  int R;                    // query heads of a unit
+  Divider page;
+  int wide;                 // rows lie 2^36 bytes or more from the pool's start
   float sl2;                // scale * log2(e)
   float* part;              // [2 grid][ROWS][D] unnormalised O
   float2* ml;               // [2 grid][ROWS] (m, l)
@@ -109,18 +120,41 @@ __device__ __forceinline__ uint32_t piece_at(int r, int c) {
   return r * ROWB + ((c ^ (r & 7)) * 16);
 }
 
-template <int D, bool E4M3>
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// Shared memory: the warps' rings of units (16 keys' rows of K or of V), the
+// queries (fp16 or bf16, rows a piece longer so that ldmatrix meets no bank
+// twice), and the warps' O at the end (rows four floats longer, likewise).
+template <int D, bool E4M3, int NB>
+struct DCfg {
+  static constexpr int R = 8 * NB;
+  static constexpr int ROWB = E4M3 ? D : 2 * D;  // bytes of a cache row
+  static constexpr int UNIT = STEP * ROWB;
+  static constexpr int QPITCH = 2 * D + 16;
+  static constexpr int JPITCH = D + 4;
+  static constexpr int JOIN_BYTES = WARPS * R * JPITCH * 4 > MAX_BATCH * 4 ? WARPS * R * JPITCH * 4 : MAX_BATCH * 4;
+  static constexpr int FIT = (224 * 1024 - R * QPITCH - JOIN_BYTES) / (WARPS * UNIT);
+  static constexpr int NU = FIT < 8 ? FIT : 8;  // units of a ring
+  static_assert(NU >= 3, "shared memory");
+  static constexpr int SMEM_BYTES = WARPS * NU * UNIT + R * QPITCH + JOIN_BYTES;
+};
+
+template <int D, bool E4M3, int NB>
 __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams p) {
-  constexpr int ROWB = E4M3 ? D : 2 * D;   // bytes of a cache row
+  using C = DCfg<D, E4M3, NB>;
+  constexpr int ROWB = C::ROWB, R = C::R, NU = C::NU;
   constexpr int PIECES = ROWB / 16;
-  constexpr int RPI = 32 / PIECES;         // rows a warp copies per instruction
-  constexpr int STAGE = 2 * STEP * ROWB;   // K rows, then V rows
-  constexpr int NST = RING_BYTES / STAGE < 6 ? RING_BYTES / STAGE : 6;
-  constexpr int NT = D / 8;                // O column tiles
-  constexpr int KS = D / 16;
+  constexpr int RPI = 32 / PIECES;  // rows a warp copies per instruction
+  constexpr int AHEAD = NU - 1;     // units copied ahead
+  constexpr int KS = D / 16;        // 16-column steps of a row
   extern __shared__ __align__(128) uint8_t smem[];
-  float* join = reinterpret_cast<float*>(smem + WARPS * NST * STAGE);  // 4 warps' O; the prefix at the start
-  __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
+  uint8_t* sQ = smem + WARPS * NU * C::UNIT;
+  float* join = reinterpret_cast<float*>(sQ + R * C::QPITCH);  // the prefix at the start
+  __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS], sm_sl2[ROWS];
   __shared__ int warp_sum[WARPS];
   __shared__ int start_b;
   __shared__ long long sh_total;
@@ -178,290 +212,376 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
   __syncthreads();  // prefix has been read
   if (w.at >= w.end) return;
 
-  // ---- the copies run NST - 1 steps ahead, the page lookups one more
-  const uint32_t ring = smem_u32(smem) + warp * (NST * STAGE);
-  Walk f = w;          // the next step to look up
-  long long row_next;  // its rows' offsets (lane r < 16: row r; -1: not read)
-  int hk_next = 0;
+  // ---- the copies run AHEAD units ahead of the products, the page lookups a
+  // step ahead of the copies.  Lane r (and r + 16) looks up row r of a step.
+  const uint32_t ring = smem_u32(smem) + warp * (NU * C::UNIT);
+  const int piece = lane % PIECES, row_of_lane = lane / PIECES;
+  Walk f = w;  // the next step to look up
   long long looked = f.at;
+  int f_hk = f.hu / p.HB;
+  const int* f_table = p.c.table + f.b * p.c.table_stride;
+  int page = 0, slot = 0, page_hk = 0;  // of the step looked up last
+  bool asked = false;                   // the row exists
   auto look_up = [&]() {
-    row_next = -1;
+    asked = false;
     if (looked < f.end) {
       const int key = f.blk * BLOCK + warp * STEP + (lane & 15);
-      hk_next = f.hu / p.HB;
+      page_hk = f_hk;
       if (key < f.len) {
-        row_next = row_offset(p.c, page_of(p.c, f.b, key), key % p.c.page_size);
-        if (row_next < 0) bad_page(p.status);
+        const int i = p.page(key);
+        slot = key - i * p.c.page_size;
+        page = __ldg(f_table + i);  // i < max_pages: len is held to what the table spans
+        asked = true;
       }
-      f.at = ++looked;
-      if (++f.blk == f.nblk) next_unit(work, f);
+      ++looked;
+      if (++f.blk == f.nblk) {
+        f.at = looked;
+        next_unit(work, f);
+        f_hk = f.hu / p.HB;
+        f_table = p.c.table + f.b * p.c.table_stride;
+      }
     }
   };
-  uint32_t put = 0;
-  auto copy_step = [&]() {
-    const uint32_t dst = ring + (put % NST) * STAGE;
-    const int c = lane % PIECES;
-    const long long head = hk_next * p.c.head_stride + c * 16;
+  uint32_t off_lo = 0, off_hi = 0, real = 0;  // of the step to copy: the row's place (16-byte pieces), which rows are read
+  long long head_off = 0;
+  auto next_rows = [&]() {
+    const bool good = asked && page >= 0 && page < p.c.num_pages;
+    if (asked && !good) bad_page(p.status);
+    const unsigned long long off = good ? (unsigned long long)(page * p.c.page_stride + slot * p.c.row_stride) >> 4 : 0ull;
+    off_lo = (uint32_t)off;
+    off_hi = (uint32_t)(off >> 32);
+    real = __ballot_sync(0xffffffffu, good);
+    head_off = page_hk * p.c.head_stride + piece * 16;
+  };
+  uint32_t put = 0;  // ring slot of the next unit
+  auto copy_unit = [&](const uint8_t* pool) {
+    const uint32_t dst = ring + put * C::UNIT;
+    put = put + 1 == NU ? 0 : put + 1;
+    const uint8_t* src = pool + head_off;
 #pragma unroll
     for (int i = 0; i < STEP / RPI; ++i) {
-      const int r = i * RPI + lane / PIECES;
-      const long long off = __shfl_sync(0xffffffffu, row_next, r);
-      const bool real = off >= 0;
-      const long long at = real ? off + head : 0;
-      cp16(dst + piece_at<ROWB>(r, c), p.c.K + at, real);
-      cp16(dst + STEP * ROWB + piece_at<ROWB>(r, c), p.c.V + at, real);
+      const int r = i * RPI + row_of_lane;
+      unsigned long long off = __shfl_sync(0xffffffffu, off_lo, r);
+      if (p.wide) off |= (unsigned long long)__shfl_sync(0xffffffffu, off_hi, r) << 32;
+      const bool read = (real >> r) & 1u;
+      cp16(dst + piece_at<ROWB>(r, piece), src + (off << 4), read);
     }
-    ++put;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto copy_k = [&]() { copy_unit(p.c.K); };
+  auto copy_v = [&]() {
+    copy_unit(p.c.V);
+    next_rows();
+    look_up();
   };
   look_up();
+  next_rows();
+  look_up();
 #pragma unroll
-  for (int i = 0; i < NST - 1; ++i) {
-    copy_step();
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    look_up();
+  for (int i = 0; i < AHEAD; ++i) {
+    if (i & 1) copy_v();
+    else copy_k();
   }
 
-  uint32_t got = 0;
+  uint32_t got = 0;  // ring slot of the next unit to use
   while (w.at < w.end) {
     // ---- a unit, or this CTA's part of it
-    const int hk = w.hu / p.HB, row0 = (w.hu % p.HB) * ROWS;
-    const int heads = min(ROWS, p.G - row0);  // rows in use
+    const int hk = w.hu / p.HB, row0 = (w.hu % p.HB) * R;
+    const int heads = min(R, p.G - row0);  // query heads in use
     const int b = w.b;
     const long long unit_begin = w.at - w.blk;
     const int nseg = (int)min((long long)(w.nblk - w.blk), w.end - w.at);
-    const long long q_first = (long long)b * p.Hq + hk * p.G + row0;  // output row of the unit's row 0
-    // queries as A fragments: rows g and g + 8
-    uint32_t qa[KS][4];
-    float sl2[2];
-    {
-      float amax[2] = {0.0f, 0.0f};
+    const long long q_first = (long long)b * p.Hq + hk * p.G + row0;  // output row of the unit's first head
+    // ---- the queries: a row per warp into shared memory
+    for (int r = warp; r < R; r += WARPS) {
+      constexpr int E = D / 32;  // values a lane
+      float x[E];
+      const __nv_bfloat16* src = p.Q + b * p.q_row + (hk * p.G + row0 + r) * p.q_head + lane * E;
+      if (r < heads) {
+        if (E == 4) {
+          const uint2 v = *reinterpret_cast<const uint2*>(src);
+          const uint32_t u[2] = {v.x, v.y};
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = g + (e & 1) * 8;
-          // bf16: columns 16 s + 2 t and + 8; 8 bits: 16 s + 4 t and + 2 (the
-          // order in which a lane finds its four values of a 16-byte piece)
-          const int col = E4M3 ? 16 * s + 4 * t + (e >> 1) * 2 : 16 * s + 2 * t + (e >> 1) * 8;
-          qa[s][e] = r < heads ? *reinterpret_cast<const uint32_t*>(p.Q + b * p.q_row +
-                                                                    (hk * p.G + row0 + r) * p.q_head + col)
-                               : 0u;
-          if (E4M3)
-            amax[e & 1] = fmaxf(amax[e & 1], fmaxf(fabsf(__uint_as_float(qa[s][e] << 16)),
-                                                   fabsf(__uint_as_float(qa[s][e] & 0xffff0000u))));
+          for (int e = 0; e < E; ++e) x[e] = __uint_as_float(e & 1 ? u[e / 2] & 0xffff0000u : u[e / 2] << 16);
+        } else {
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(src);
+          x[0] = __uint_as_float(u << 16);
+          x[1] = __uint_as_float(u & 0xffff0000u);
         }
-      sl2[0] = sl2[1] = p.sl2;
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = 0.0f;
+      }
+      float sl2 = p.sl2;
       if (E4M3) {
         // bf16 reaches further than fp16: each row is scaled by the power of
         // two that brings its largest entry into [1, 2).  Entries below 2^-14 of
         // that lose bits that the row's sum cannot show.
-        const float ks = __ldg(p.c.k_scale + hk);
+        float amax = 0.0f;
 #pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          amax[z] = fmaxf(amax[z], __shfl_xor_sync(0xffffffffu, amax[z], 1));
-          amax[z] = fmaxf(amax[z], __shfl_xor_sync(0xffffffffu, amax[z], 2));
-          const int e = max(-126, min(126, (int)(__float_as_uint(amax[z]) >> 23) - 127));
-          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-          sl2[z] = p.sl2 * ks * __uint_as_float((uint32_t)(127 + e) << 23);
+        for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[e]));
 #pragma unroll
-          for (int s = 0; s < KS; ++s)
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const int e2 = max(-126, min(126, (int)(__float_as_uint(amax) >> 23) - 127));
+        const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+        sl2 = p.sl2 * __ldg(p.c.k_scale + hk) * __uint_as_float((uint32_t)(127 + e2) << 23);
 #pragma unroll
-            for (int e2 = 0; e2 < 2; ++e2) {
-              const uint32_t x = qa[s][z + 2 * e2];
-              qa[s][z + 2 * e2] = pack2<true>(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
-            }
-        }
+        for (int e = 0; e < E; ++e) x[e] *= down;
       }
-    }
-    float o[NT][4];
+      if (lane == 0) sm_sl2[r] = sl2;
+      // 8 bits: within 16 columns in the order in which a lane finds its four
+      // values of a piece (columns 4 t, 4 t + 1 at 2 t, and 4 t + 2, 4 t + 3 at 2 t + 8)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-
-    for (int step = 0; step < nseg; ++step, ++got) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
-      __syncwarp();
-      // the stage this step's copies go to was read out in the step before
-      copy_step();
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      look_up();
-      const uint32_t sK = ring + (got % NST) * STAGE, sV = sK + STEP * ROWB;
-      const int key0 = (w.blk + step) * BLOCK + warp * STEP;
-      const int valid = w.len - key0;  // keys of this step that exist (may be <= 0)
-      if (valid <= 0) continue;
-      // ---- S = Q K^T: two tiles of eight keys
-      float s[2][4] = {};
-      {
-        const int mi = lane >> 3, kr = (mi >> 1) * 8 + (lane & 7);  // ldmatrix: key half, piece parity
-#pragma unroll
-        for (int c = 0; c < PIECES; c += 2) {
-          uint32_t r[4];
-          ldsm4(r, sK + piece_at<ROWB>(kr, c + (mi & 1)));
-          if (E4M3) {  // a piece is 16 columns: one product each
-            mma<true>(s[0], qa[c], widen(r[0]), widen(r[0] >> 16));
-            mma<true>(s[1], qa[c], widen(r[2]), widen(r[2] >> 16));
-            mma<true>(s[0], qa[c + 1], widen(r[1]), widen(r[1] >> 16));
-            mma<true>(s[1], qa[c + 1], widen(r[3]), widen(r[3] >> 16));
-          } else {
-            mma<false>(s[0], qa[c / 2], r[0], r[1]);
-            mma<false>(s[1], qa[c / 2], r[2], r[3]);
-          }
-        }
-      }
-      // ---- online softmax; a lane has keys 2t, 2t + 1 (+ 8) of rows g, g + 8
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[j][e] = j * 8 + 2 * t + (e & 1) < valid ? s[j][e] * sl2[e >> 1] : -INFINITY;
-      if (p.scores) {
-#pragma unroll
-        for (int z = 0; z < 2; ++z)
-          if (g + 8 * z < heads) {
-            float* row = p.scores + (q_first + g + 8 * z) * p.pitch + key0 + 2 * t;
-            *reinterpret_cast<float2*>(row) = make_float2(s[0][2 * z], s[0][2 * z + 1]);
-            *reinterpret_cast<float2*>(row + 8) = make_float2(s[1][2 * z], s[1][2 * z + 1]);
-          }
-      }
-      float alpha[2];
-      uint32_t pa[4];
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        float mx = fmaxf(fmaxf(s[0][2 * z], s[0][2 * z + 1]), fmaxf(s[1][2 * z], s[1][2 * z + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        mx = fmaxf(mx, m[z]);
-        const float ref = mx == -INFINITY ? 0.0f : mx;  // every score so far -inf: P = 0
-        alpha[z] = ex2_approx(m[z] - ref);
-        m[z] = mx;
-        const float p0 = ex2_approx(s[0][2 * z] - ref), p1 = ex2_approx(s[0][2 * z + 1] - ref);
-        const float p2 = ex2_approx(s[1][2 * z] - ref), p3 = ex2_approx(s[1][2 * z + 1] - ref);
-        l[z] = l[z] * alpha[z] + ((p0 + p1) + (p2 + p3));
-        pa[z] = pack2<E4M3>(p0, p1);
-        pa[z + 2] = pack2<E4M3>(p2, p3);
-      }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          o[n][0] *= alpha[0];
-          o[n][1] *= alpha[0];
-          o[n][2] *= alpha[1];
-          o[n][3] *= alpha[1];
-        }
-      }
-      // ---- O += P V (ldmatrix transposed: keys 0..7 and 8..15 of two pieces)
-      {
-        const int mi = lane >> 3, kr = (mi & 1) * 8 + (lane & 7);
-#pragma unroll
-        for (int c = 0; c < PIECES; c += 2) {
-          uint32_t r[4];
-          ldsm4_t(r, sV + piece_at<ROWB>(kr, c + (mi >> 1)));
-          if (E4M3) {
-            // bytes (key, col), (key, col + 1), (key + 1, col), (key + 1, col + 1):
-            // even columns make one tile, odd ones the next
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint32_t x0 = __byte_perm(r[2 * u], 0, 0x3120), x1 = __byte_perm(r[2 * u + 1], 0, 0x3120);
-              mma<true>(o[2 * (c + u)], pa, widen(x0), widen(x1));
-              mma<true>(o[2 * (c + u) + 1], pa, widen(x0 >> 16), widen(x1 >> 16));
-            }
-          } else {
-            mma<false>(o[c], pa, r[0], r[1]);
-            mma<false>(o[c + 1], pa, r[2], r[3]);
-          }
-        }
-      }
-    }
-
-    // ---- join the eight warps
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      l[z] += __shfl_xor_sync(0xffffffffu, l[z], 1);
-      l[z] += __shfl_xor_sync(0xffffffffu, l[z], 2);
-      if (t == 0) {
-        sm_m[warp][g + 8 * z] = m[z];
-        sm_l[warp][g + 8 * z] = l[z];
+      for (int e = 0; e < E; e += 2) {
+        const int col = lane * E + e, in = col & 15;
+        const int at = E4M3 ? (col & ~15) + ((in & 2) ? 8 : 0) + (in >> 2) * 2 : col;
+        *reinterpret_cast<uint32_t*>(sQ + r * C::QPITCH + at * 2) = pack2<E4M3>(x[e], x[e + 1]);
       }
     }
     __syncthreads();
-    float M[2], L[2];
+    // B operands: head g, columns 2 t, 2 t + 1 (+ 8) of each 16
+    const uint32_t q_at = smem_u32(sQ) + (lane & 7) * C::QPITCH + (lane >> 3) * 16;
+    uint32_t qb[NB == 1 ? KS / 2 : 1][4];
+    if (NB == 1) {
 #pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      M[z] = -INFINITY;
-#pragma unroll
-      for (int v = 0; v < WARPS; ++v) M[z] = fmaxf(M[z], sm_m[v][g + 8 * z]);
-      const float ref = M[z] == -INFINITY ? 0.0f : M[z];
-      L[z] = 0.0f;
-#pragma unroll
-      for (int v = 0; v < WARPS; ++v) L[z] += sm_l[v][g + 8 * z] * ex2_approx(sm_m[v][g + 8 * z] - ref);
-      const float f0 = ex2_approx(m[z] - ref);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        o[n][2 * z] *= f0;
-        o[n][2 * z + 1] *= f0;
-      }
+      for (int s = 0; s < KS / 2; ++s) ldsm4(qb[NB == 1 ? s : 0], q_at + s * 64);
     }
-    // columns of a lane in tile n: bf16 8 n + 2 t, + 1; 8 bits: tiles 2i and
-    // 2i + 1 hold the even and odd columns of piece i, 16 i + 2 (2t, 2t + 1) (+ 1)
+    float sl2[NB][2];
 #pragma unroll
-    for (int half = WARPS / 2; half > 0; half >>= 1) {
-      float4* buf = reinterpret_cast<float4*>(join) + (warp % half) * (NT * 32) + lane;
-      if (warp >= half && warp < 2 * half)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) buf[n * 32] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
-      __syncthreads();
-      if (warp < half)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float4 x = buf[n * 32];
-          o[n][0] += x.x;
-          o[n][1] += x.y;
-          o[n][2] += x.z;
-          o[n][3] += x.w;
-        }
-      __syncthreads();
+    for (int n = 0; n < NB; ++n) {
+      sl2[n][0] = sm_sl2[n * 8 + 2 * t];
+      sl2[n][1] = sm_sl2[n * 8 + 2 * t + 1];
     }
-    if (warp == 0) {
-      const bool whole = nseg == w.nblk;
-      const float vs = E4M3 ? __ldg(p.c.v_scale + hk) : 1.0f;
-      const int slot = part_slot(cta, begin, unit_begin);
+    // O^T: tile i, rows g and g + 8 (bf16: columns 16 i + g, + 8 of the head; 8
+    // bits: 16 i + 2 g, + 1), heads 8 n + 2 t, + 1
+    float o[KS][NB][4];
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const int r = g + 8 * z;
-        if (r >= heads) continue;
-        const float inv = L[z] > 0.0f ? vs / L[z] : L[z] == 0.0f ? 0.0f : L[z];
-        float* prow = p.part + ((long long)slot * ROWS + r) * D;
-        __nv_bfloat16* orow = p.O + (q_first + r) * D;
+    for (int i = 0; i < KS; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; n += E4M3 ? 2 : 1) {
-          if (E4M3) {
-            // four neighbouring columns: even, odd, even, odd
-            const float x0 = o[n][2 * z], x1 = o[n + 1][2 * z], x2 = o[n][2 * z + 1], x3 = o[n + 1][2 * z + 1];
-            const int col = 8 * n + 4 * t;
-            if (whole)
-              *reinterpret_cast<uint2*>(orow + col) = make_uint2(pack2<false>(x0 * inv, x1 * inv), pack2<false>(x2 * inv, x3 * inv));
-            else
-              *reinterpret_cast<float4*>(prow + col) = make_float4(x0 * vs, x1 * vs, x2 * vs, x3 * vs);
+      for (int n = 0; n < NB; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
+    float m[NB][2], l[NB][2];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+    }
+
+    for (int step = 0; step < nseg; ++step) {
+      const int key0 = (w.blk + step) * BLOCK + warp * STEP;
+      const int valid = w.len - key0;  // keys of this step that exist (may be <= 0)
+      asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+      __syncwarp();
+      // the slot this unit goes to was read out in the step before
+      if (AHEAD & 1) copy_v();
+      else copy_k();
+      const uint32_t sK = ring + got * C::UNIT;
+      got = got + 1 == NU ? 0 : got + 1;
+      uint32_t pb[NB][2];  // P^T as B operand
+      if (valid > 0) {
+        // ---- S^T = K Q^T
+        float c[NB][2][4] = {};  // two chains of products
+        const int mi = lane >> 3, kr = (mi & 1) * 8 + (lane & 7);
+#pragma unroll
+        for (int s = 0; s < KS; s += 2) {
+          uint32_t q4[NB][4];
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            if (NB == 1) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) q4[n][e] = qb[NB == 1 ? s / 2 : 0][e];
+            } else {
+              ldsm4(q4[n], q_at + n * 8 * C::QPITCH + s * 32);
+            }
+          }
+          uint32_t a0[4], a1[4];
+          if (E4M3) {  // a piece is 16 columns
+            uint32_t r[4];
+            ldsm4(r, sK + piece_at<ROWB>(kr, s + (mi >> 1)));
+            a0[0] = widen(r[0]);
+            a0[1] = widen(r[1]);
+            a0[2] = widen(r[0] >> 16);
+            a0[3] = widen(r[1] >> 16);
+            a1[0] = widen(r[2]);
+            a1[1] = widen(r[3]);
+            a1[2] = widen(r[2] >> 16);
+            a1[3] = widen(r[3] >> 16);
           } else {
-            const int col = 8 * n + 2 * t;
-            if (whole)
-              *reinterpret_cast<uint32_t*>(orow + col) = pack2<false>(o[n][2 * z] * inv, o[n][2 * z + 1] * inv);
-            else
-              *reinterpret_cast<float2*>(prow + col) = make_float2(o[n][2 * z], o[n][2 * z + 1]);
+            ldsm4(a0, sK + piece_at<ROWB>(kr, 2 * s + (mi >> 1)));
+            ldsm4(a1, sK + piece_at<ROWB>(kr, 2 * s + 2 + (mi >> 1)));
+          }
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            mma<E4M3>(c[n][0], a0, q4[n][0], q4[n][1]);
+            mma<E4M3>(c[n][1], a1, q4[n][2], q4[n][3]);
           }
         }
-        if (t == 0) {
-          if (whole) p.LSE[q_first + r] = (M[z] + log2f(L[z])) * LN2;
-          else p.ml[(long long)slot * ROWS + r] = make_float2(M[z], L[z]);
+        // ---- online softmax; a lane has keys g, g + 8 of heads 2 t, 2 t + 1
+        float x[NB][4];
+        bool above = false;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[n][e] = g + (e >> 1) * 8 < valid ? (c[n][0][e] + c[n][1][e]) * sl2[n][e & 1] : -INFINITY;
+          if (p.scores) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int h = n * 8 + 2 * t + e;
+              if (h < heads) {
+                float* row = p.scores + (q_first + h) * p.pitch + key0 + g;
+                row[0] = x[n][e];
+                row[8] = x[n][e + 2];
+              }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) above |= fmaxf(x[n][e], x[n][e + 2]) > m[n][e] + SLACK;
+        }
+        if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(x[n][e], x[n][e + 2]);
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              mx = fmaxf(mx, m[n][e]);
+              const float down = ex2_approx(m[n][e] - (mx == -INFINITY ? 0.0f : mx));
+              m[n][e] = mx;
+              l[n][e] *= down;
+#pragma unroll
+              for (int i = 0; i < KS; ++i) {
+                o[i][n][e] *= down;
+                o[i][n][e + 2] *= down;
+              }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          const float r0 = m[n][0] == -INFINITY ? 0.0f : m[n][0];  // every score so far -inf: P = 0
+          const float r1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
+          const float p0 = ex2_approx(x[n][0] - r0), p1 = ex2_approx(x[n][1] - r1);
+          const float p2 = ex2_approx(x[n][2] - r0), p3 = ex2_approx(x[n][3] - r1);
+          l[n][0] += p0 + p2;
+          l[n][1] += p1 + p3;
+          pb[n][0] = transpose8x8(pack2<E4M3>(p0, p1));
+          pb[n][1] = transpose8x8(pack2<E4M3>(p2, p3));
+        }
+      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+      __syncwarp();
+      if (AHEAD & 1) copy_k();
+      else copy_v();
+      const uint32_t sV = ring + got * C::UNIT;
+      got = got + 1 == NU ? 0 : got + 1;
+      if (valid > 0) {
+        // ---- O^T += V^T P^T (ldmatrix transposed)
+        const int mi = lane >> 3;
+#pragma unroll
+        for (int i = 0; i < KS; i += 2) {
+          uint32_t a0[4], a1[4];
+          if (E4M3) {
+            // bytes (key, col), (key, col + 1), (key + 1, col), (key + 1, col + 1): the
+            // even columns are rows g of the tile, the odd ones rows g + 8
+            uint32_t r[4];
+            ldsm4_t(r, sV + piece_at<ROWB>((mi & 1) * 8 + (lane & 7), i + (mi >> 1)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[e] = __byte_perm(r[e], 0, 0x3120);
+            a0[0] = widen(r[0]);
+            a0[1] = widen(r[0] >> 16);
+            a0[2] = widen(r[1]);
+            a0[3] = widen(r[1] >> 16);
+            a1[0] = widen(r[2]);
+            a1[1] = widen(r[2] >> 16);
+            a1[2] = widen(r[3]);
+            a1[3] = widen(r[3] >> 16);
+          } else {
+            const int kr = (mi >> 1) * 8 + (lane & 7);
+            ldsm4_t(a0, sV + piece_at<ROWB>(kr, 2 * i + (mi & 1)));
+            ldsm4_t(a1, sV + piece_at<ROWB>(kr, 2 * i + 2 + (mi & 1)));
+          }
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            mma<E4M3>(o[i][n], a0, pb[n][0], pb[n][1]);
+            mma<E4M3>(o[i + 1][n], a1, pb[n][0], pb[n][1]);
+          }
+        }
+      }
+    }
+
+    // ---- join the eight warps, in their order
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+        if (g == 0) {
+          sm_m[warp][n * 8 + 2 * t + e] = m[n][e];
+          sm_l[warp][n * 8 + 2 * t + e] = l[n][e];
+        }
+      }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = n * 8 + 2 * t + e;
+        float M = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < WARPS; ++v) M = fmaxf(M, sm_m[v][h]);
+        const float f0 = ex2_approx(m[n][e] - (M == -INFINITY ? 0.0f : M));
+        float* row = join + (warp * R + h) * C::JPITCH;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          if (E4M3) {
+            *reinterpret_cast<float2*>(row + 16 * i + 2 * g) = make_float2(o[i][n][e] * f0, o[i][n][e + 2] * f0);
+          } else {
+            row[16 * i + g] = o[i][n][e] * f0;
+            row[16 * i + g + 8] = o[i][n][e + 2] * f0;
+          }
+        }
+      }
+    __syncthreads();
+    {
+      const bool whole = nseg == w.nblk;
+      const float vs = E4M3 ? __ldg(p.c.v_scale + hk) : 1.0f;
+      const int part = part_slot(cta, begin, unit_begin);
+      for (int k = tid; k < heads * (D / 4); k += THREADS) {
+        const int h = k / (D / 4), col = k % (D / 4) * 4;
+        float M = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int v = 0; v < WARPS; ++v) M = fmaxf(M, sm_m[v][h]);
+        const float ref = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+        for (int v = 0; v < WARPS; ++v) L += sm_l[v][h] * ex2_approx(sm_m[v][h] - ref);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < WARPS; ++v) {
+          const float4 y = *reinterpret_cast<const float4*>(join + (v * R + h) * C::JPITCH + col);
+          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        if (whole) {
+          const float inv = L > 0.0f ? vs / L : L == 0.0f ? 0.0f : L;
+          *reinterpret_cast<uint2*>(p.O + (q_first + h) * D + col) =
+              make_uint2(pack2<false>(x.x * inv, x.y * inv), pack2<false>(x.z * inv, x.w * inv));
+          if (col == 0) p.LSE[q_first + h] = (M + log2f(L)) * LN2;
+        } else {
+          *reinterpret_cast<float4*>(p.part + ((long long)part * ROWS + h) * D + col) =
+              make_float4(x.x * vs, x.y * vs, x.z * vs, x.w * vs);
+          if (col == 0) p.ml[(long long)part * ROWS + h] = make_float2(M, L);
         }
       }
       // the unit begins here and goes on: the join kernel's block `cta` joins it
-      if (lane == 0 && !whole && w.blk == 0) {
+      if (tid == 0 && !whole && w.blk == 0) {
         const int last = owner(total, grid, unit_begin + w.nblk - 1);
-        p.desc[cta] = make_int4(b, w.hu, slot, last - cta + 1);
+        p.desc[cta] = make_int4(b, w.hu, part, last - cta + 1);
       }
     }
-    __syncthreads();  // sm_m, sm_l
+    // (sm_m, sm_l and the joined rows are written again only after the next
+    // unit's barrier behind its queries, or behind its products)
     w.at += nseg;
     w.blk += nseg;
     if (w.blk == w.nblk) next_unit(work, w);
@@ -477,8 +597,8 @@ __global__ void __launch_bounds__(D) join_kernel(const DecodeParams p, int rows)
   const int c0 = blockIdx.x / rows, r = blockIdx.x % rows, col = threadIdx.x;
   const int4 u = p.desc[c0];
   if (u.x < 0) return;
-  const int hk = u.y / p.HB, row0 = (u.y % p.HB) * ROWS;
-  if (r >= min(ROWS, p.G - row0)) return;
+  const int hk = u.y / p.HB, row0 = (u.y % p.HB) * p.R;
+  if (r >= min(p.R, p.G - row0)) return;
   // in CTAs after c0 the unit comes first: slot 2 c
   const int first = u.z;
   float M = -INFINITY;
@@ -498,7 +618,8 @@ __global__ void __launch_bounds__(D) join_kernel(const DecodeParams p, int rows)
   if (col == 0) p.LSE[row] = (M + log2f(L)) * LN2;
 }
 
-// A[b, hk, j] (+)= sum over the group of 2^(s_j - LSE log2 e).
+// A[b, hk, j] (+)= sum over the group of 2^(s_j - LSE log2 e): four keys a
+// thread, four heads' scores in flight.
 constexpr int W_THREADS = 256;
 __global__ void __launch_bounds__(W_THREADS) weights_kernel(const DecodeParams p, float* A, long long a_batch,
                                                             long long a_head, int accumulate, int chunks) {
@@ -507,14 +628,24 @@ __global__ void __launch_bounds__(W_THREADS) weights_kernel(const DecodeParams p
   const int bh = blockIdx.x / chunks, b = bh / p.Hkv, hk = bh % p.Hkv;
   const int len = clamp_len(p.c, __ldg(p.lens + b));
   const long long first = (long long)b * p.Hq + hk * p.G;
-  for (long long j = (long long)(blockIdx.x % chunks) * W_THREADS + threadIdx.x; j < len;
-       j += (long long)chunks * W_THREADS) {
-    float sum = 0.0f;
+  for (long long j = 4 * ((long long)(blockIdx.x % chunks) * W_THREADS + threadIdx.x); j < len;
+       j += 4LL * chunks * W_THREADS) {
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int r = 0; r < p.G; ++r)
-      sum += ex2_approx(p.scores[(first + r) * p.pitch + j] - __ldg(p.LSE + first + r) * LOG2E);
+    for (int r = 0; r < p.G; ++r) {
+      // (rows are 16-byte aligned, and end on a whole step behind the last key)
+      const float4 s = *reinterpret_cast<const float4*>(p.scores + (first + r) * p.pitch + j);
+      const float lse = __ldg(p.LSE + first + r) * LOG2E;
+      sum.x += ex2_approx(s.x - lse);
+      sum.y += ex2_approx(s.y - lse);
+      sum.z += ex2_approx(s.z - lse);
+      sum.w += ex2_approx(s.w - lse);
+    }
     float* a = A + b * a_batch + hk * a_head + j;
-    *a = accumulate ? *a + sum : sum;
+    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (j + e < len) a[e] = accumulate ? a[e] + v[e] : v[e];
   }
 }
 
@@ -539,15 +670,14 @@ size_t paged_decode_workspace_bytes(int B, int Hq, int d, long long cap, bool we
   return paged::layout(B, Hq, d, cap, weights, num_sms()).total;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NB>
 static fa_status launch_d(paged::DecodeParams p, int B, const PagedDecode& a, int grid, cudaStream_t s) {
   using namespace paged;
-  constexpr int STAGE = 2 * STEP * (E4M3 ? D : 2 * D);
-  constexpr int NST = RING_BYTES / STAGE < 6 ? RING_BYTES / STAGE : 6;
-  constexpr int smem = WARPS * NST * STAGE + WARPS / 2 * ROWS * D * 4;
-  static_assert(smem + 2048 <= 227 * 1024 && WARPS / 2 * ROWS * D * 4 >= MAX_BATCH * 4, "shared memory");
+  constexpr int smem = DCfg<D, E4M3, NB>::SMEM_BYTES;
+  static_assert(smem + 2048 <= 227 * 1024, "shared memory");
+  auto kern = partial_kernel<D, E4M3, NB>;
   static std::atomic<uint64_t> done{0};
-  if (!allow_smem(done, (const void*)partial_kernel<D, E4M3>, smem)) return FA_ERR_CUDA;
+  if (!allow_smem(done, (const void*)kern, smem)) return FA_ERR_CUDA;
   const int* lens = p.lens;
   const int* table = p.c.table;
   const __nv_bfloat16* Q = p.Q;
@@ -562,11 +692,11 @@ static fa_status launch_d(paged::DecodeParams p, int B, const PagedDecode& a, in
     p.O = O + (long long)b0 * p.Hq * D;
     p.LSE = LSE + (long long)b0 * p.Hq;
     if (scores) p.scores = scores + (long long)b0 * p.Hq * p.pitch;
-    if (!launch_early(partial_kernel<D, E4M3>, (unsigned)grid, THREADS, smem, s, p)) return FA_ERR_CUDA;
-    const int rows = p.G < ROWS ? p.G : ROWS;
+    if (!launch_early(kern, (unsigned)grid, THREADS, smem, s, p)) return FA_ERR_CUDA;
+    const int rows = p.G < p.R ? p.G : p.R;
     if (!launch_early(join_kernel<D>, (unsigned)(grid * rows), D, 0, s, p, rows)) return FA_ERR_CUDA;
     if (scores) {
-      long long chunks = (p.pitch + 4 * W_THREADS - 1) / (4 * W_THREADS);
+      long long chunks = (p.pitch + 4 * W_THREADS - 1) / (4 * W_THREADS);  // four keys a thread
       if (chunks > 64) chunks = 64;
       if (!launch_early(weights_kernel, (unsigned)(p.B * p.Hkv * chunks), W_THREADS, 0, s, p, a.W + b0 * a.w_batch,
                         a.w_batch, a.w_head, a.accumulate, (int)chunks))
@@ -592,7 +722,10 @@ fa_status launch_paged_decode(const PagedCache& c, const PagedDecode& a, cudaStr
   p.Hq = a.Hq;
   p.Hkv = c.Hkv;
   p.G = a.Hq / c.Hkv;
-  p.HB = (p.G + paged::ROWS - 1) / paged::ROWS;
+  p.R = p.G <= 8 ? 8 : 16;
+  p.HB = (p.G + p.R - 1) / p.R;
+  p.page = paged::make_divider(c.page_size);
+  p.wide = ((c.num_pages - 1) * c.page_stride + (c.page_size - 1) * c.row_stride) * c.elem >= (1ll << 36);
   p.sl2 = a.scale_log2;
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
@@ -602,9 +735,13 @@ fa_status launch_paged_decode(const PagedCache& c, const PagedDecode& a, cudaStr
   p.O = static_cast<__nv_bfloat16*>(a.O);
   p.LSE = a.LSE;
   p.status = st;
-  if (c.elem == 1)
-    return c.d == 64 ? launch_d<64, true>(p, c.B, a, grid, s) : launch_d<128, true>(p, c.B, a, grid, s);
-  return c.d == 64 ? launch_d<64, false>(p, c.B, a, grid, s) : launch_d<128, false>(p, c.B, a, grid, s);
+  auto launch = [&](auto nb) {
+    constexpr int NB = decltype(nb)::value;
+    if (c.elem == 1)
+      return c.d == 64 ? launch_d<64, true, NB>(p, c.B, a, grid, s) : launch_d<128, true, NB>(p, c.B, a, grid, s);
+    return c.d == 64 ? launch_d<64, false, NB>(p, c.B, a, grid, s) : launch_d<128, false, NB>(p, c.B, a, grid, s);
+  };
+  return p.R == 8 ? launch(std::integral_constant<int, 1>()) : launch(std::integral_constant<int, 2>());
 }
 
 }  // namespace fa

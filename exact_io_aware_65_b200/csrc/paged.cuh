@@ -40,6 +40,22 @@ __host__ __device__ __forceinline__ int page_of(const Cache& c, int b, long long
   return ld_ro(c.table + b * c.table_stride + i);
 }
 
+// Division of n < 2^31 by a number fixed for the launch: with 2^(s-1) < d <= 2^s
+// and mul = ceil(2^(31+s) / d), n mul / 2^(31+s) exceeds n / d by less than
+// n d / (d 2^(31+s)) < 1 / d, and so has the same whole part.
+struct Divider {
+  uint32_t mul;
+  int shift;
+  __host__ __device__ __forceinline__ int operator()(int n) const {
+    return (int)(((unsigned long long)(uint32_t)n * mul) >> shift);
+  }
+};
+inline Divider make_divider(int d) {
+  int s = 0;
+  while ((1ll << s) < d) ++s;
+  return Divider{(uint32_t)(((1ull << (31 + s)) + d - 1) / d), 31 + s};
+}
+
 // Records a page index outside the pool.
 __device__ __forceinline__ void bad_page(uint32_t* status) { atomicCAS(status, FA_DEV_OK, FA_DEV_ERR_BOUNDS); }
 
