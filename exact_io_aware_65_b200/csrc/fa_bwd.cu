@@ -204,7 +204,6 @@ template <int D>
 __global__ void __launch_bounds__(256) packed_prep_kernel(const PackedArgs a) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane / LPR, li = lane % LPR;
-  pdl_wait();
   const int slot = blockIdx.x / a.pk.Hq, h = blockIdx.x % a.pk.Hq;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.sched = 0u;
   const int b = pack::sequence_of_slot(a.pk, slot);
@@ -1333,7 +1332,7 @@ static fa_status launch_bwd_packed_d(const PackedProblem& pr, const CUtensorMap&
   a.scale = pr.scale;
   a.status = st;
   const unsigned blocks = (unsigned)(pack::slots(k.Tq, k.B) * k.Hq);
-  if (!launch_early(bwd::packed_prep_kernel<D>, blocks, 256, 0, s, a)) return FA_ERR_CUDA;
+  if (!launch(bwd::packed_prep_kernel<D>, blocks, 256, 0, s, a)) return FA_ERR_CUDA;
   if (k.Tk > 0) {
     bwd::Params p = {};
     p.pk = k;
@@ -1364,17 +1363,16 @@ static fa_status launch_bwd_packed_d(const PackedProblem& pr, const CUtensorMap&
     auto kern = bwd::main_kernel<D, PACKED>;
     static std::atomic<uint64_t> done{0};
     if (!allow_smem(done, (const void*)kern, smem)) return FA_ERR_CUDA;
-    // (set up behind the kernel before, this one and the next were slower by 2%:
-    // 1423 against 1378 us for 6100 + 8192 tokens, 52 against 50 us for 3440)
     const int sms = num_sms();
-    kern<<<p.n_items < sms ? p.n_items : sms, bwd::NUM_THREADS, smem, s>>>(mQ, mK, mV, mdO, mdK, mdV, p);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (!launch(kern, (unsigned)(p.n_items < sms ? p.n_items : sms), bwd::NUM_THREADS, smem, s, mQ, mK, mV, mdO, mdK, mdV, p))
+      return FA_ERR_CUDA;
   }
   const long long add = part ? ((long long)2 * k.Tk * k.Hkv * (D / 8) + 255) / 256 : 0;
   const unsigned dq_blocks = k.Tq > 0 ? blocks * (D / 32) : 0;
   const unsigned more = (unsigned)(add < (1 << 20) ? add : (1 << 20));
-  if (dq_blocks + more > 0) bwd::packed_convert_kernel<D><<<dq_blocks + more, 256, 0, s>>>(a, dq_blocks);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  if (dq_blocks + more > 0 && !launch(bwd::packed_convert_kernel<D>, dq_blocks + more, 256, 0, s, a, dq_blocks))
+    return FA_ERR_CUDA;
+  return FA_OK;
 }
 
 fa_status launch_bwd_packed(const PackedProblem& pr, const Rows& Q, const Rows& K, const Rows& V, const Rows& O,

@@ -178,11 +178,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   tc_fence_after();
 
-  if (MODE == PACKED) {
-    pdl_wait();
-    pdl_next();
-  }
-
   const uint32_t tmem = tmem_base_sh;
   const WaitCtx w{p.timeout_ns, &abort_flag, p.status};
 
@@ -904,7 +899,7 @@ fa_status launch_fwd_packed(const PackedProblem& pr, const Rows& Q, const Rows& 
   static std::atomic<uint64_t> done[2];  // d = 64, 128
   auto run = [&](auto kern, int smem) -> bool {
     return allow_smem(done[pr.d == 128], (const void*)kern, smem) &&
-           launch_early(kern, (unsigned)grid, fwd::NUM_THREADS, smem, s, mQ, mK, mV, mO, p);
+           launch(kern, (unsigned)grid, fwd::NUM_THREADS, smem, s, mQ, mK, mV, mO, p);
   };
   if (!(dual ? run(fwd::fwd_kernel<64, PACKED, 2>, fwd::Cfg<64, 2>::SMEM_BYTES)
              : run(fwd::fwd_kernel<128, PACKED, 1>, fwd::Cfg<128, 1>::SMEM_BYTES)))

@@ -64,21 +64,10 @@ bool make_map_bf16_2d(CUtensorMap* map, const void* base, int rows, int cols, in
 // (`done` is the kernel's own, one bit per device).
 bool allow_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes);
 
-// Launches a kernel that may be set up while the kernel before it in the stream
-// still runs: it calls pdl_wait() before it reads or writes anything.
 template <typename... P, typename... A>
-inline bool launch_early(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess;
+inline bool launch(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  kernel<<<grid, threads, smem, s>>>(P(args)...);
+  return cudaGetLastError() == cudaSuccess;
 }
 
 uint64_t wait_timeout_ns();

@@ -29,6 +29,7 @@ struct AppendParams {
   const int* cu;
   const int* lens;
   int B, T, Hkv;
+  Divider page;
   uint32_t* status;
 };
 
@@ -56,43 +57,82 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// A warp per (token, K or V): 16 bytes of the input a lane.
+// x / s from r, the correctly rounded 1 / s: with the exact remainder of the
+// first quotient, the second is x / s correctly rounded (Markstein's theorem,
+// "Computation of elementary functions on the IBM RISC System/6000", 1990).  It
+// holds while nothing on the way under- or overflows; `plain` scales are those
+// for which no bf16 x that is not held at 448 anyway, nor rounded to zero, can.
+__device__ __forceinline__ float divide(float x, float s, float r, bool plain) {
+  if (!plain) return __fdiv_rn(x, s);
+  const float q = __fmul_rn(x, r);
+  return q == 0.0f ? q : __fmaf_rn(__fmaf_rn(-q, s, x), r, q);  // (a zero keeps its sign)
+}
+
+// A warp per (token, K or V): 16 bytes of the input a lane, four pieces of it in
+// flight while the row's place is looked up (a chain of dependent loads: the
+// sequence, its length, the page).
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendParams p) {
-  pdl_wait();
-  pdl_next();
   const int lane = threadIdx.x & 31;
   const long long unit = (long long)blockIdx.x * (APPEND_THREADS / 32) + (threadIdx.x >> 5);
   const int t = (int)(unit >> 1), kv = (int)(unit & 1);
   if (t >= p.T) return;
+  constexpr int CH = D / 8;  // 16-byte pieces of a head's row
+  constexpr int N = 4;
+  const int pieces = p.Hkv * CH;
+  const __nv_bfloat16* src = kv ? p.V + t * p.v_row : p.K + t * p.k_row;
+  const long long src_head = kv ? p.v_head : p.k_head;
+  const float* scale = kv ? p.c.v_scale : p.c.k_scale;
+  uint4 x[N];
+  float s[N];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = i0 + 32 * k, h = i / CH, c = i % CH;
+      if (i < pieces) {
+        x[k] = *reinterpret_cast<const uint4*>(src + h * src_head + c * 8);
+        if (E4M3) s[k] = __ldg(scale + h);
+      }
+    }
+  };
+  load(lane);
   const int b = find_sequence(p.cu, p.B, t);
   if (b < 0 || t >= __ldg(p.cu + b + 1)) return;  // behind the last sequence
   const int held = __ldg(p.lens + b);
   const long long pos = held + (long long)t - __ldg(p.cu + b);
-  const long long off = held < 0 ? -1 : row_offset(p.c, page_of(p.c, b, pos), (int)(pos % p.c.page_size));
+  long long off = -1;
+  if (held >= 0 && pos < (long long)p.c.max_pages * p.c.page_size) {
+    const int i = p.page((int)pos);
+    off = row_offset(p.c, __ldg(p.c.table + b * p.c.table_stride + i), (int)pos - i * p.c.page_size);
+  }
   if (off < 0) {
     if (lane == 0) bad_page(p.status);
     return;
   }
-  constexpr int CH = D / 8;  // 16-byte pieces of a head's row
-  const __nv_bfloat16* src = kv ? p.V + t * p.v_row : p.K + t * p.k_row;
-  const long long src_head = kv ? p.v_head : p.k_head;
   uint8_t* dst = (kv ? p.c.V : p.c.K) + off;
-  const float* scale = kv ? p.c.v_scale : p.c.k_scale;
-#pragma unroll 4
-  for (int i = lane; i < p.Hkv * CH; i += 32) {
-    const int h = i / CH, c = i % CH;
-    const uint4 x = *reinterpret_cast<const uint4*>(src + h * src_head + c * 8);
-    if (E4M3) {
-      const float s = __ldg(scale + h);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t q[4];
+  for (int i0 = lane; i0 < pieces; i0 += 32 * N) {
+    if (i0 != lane) load(i0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        q[e] = e4m3x2(__fdiv_rn(__uint_as_float(w[e] << 16), s), __fdiv_rn(__uint_as_float(w[e] & 0xffff0000u), s));
-      *reinterpret_cast<uint2*>(dst + h * p.c.head_stride + c * 8) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-    } else {
-      *reinterpret_cast<uint4*>(dst + h * p.c.head_stride + c * 16) = x;
+    for (int k = 0; k < N; ++k) {
+      const int i = i0 + 32 * k, h = i / CH, c = i % CH;
+      if (i >= pieces) break;
+      if (E4M3) {
+        const bool plain = s[k] > 0x1p-60f && s[k] < 0x1p60f;
+        const float r = __frcp_rn(s[k]);
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        uint32_t q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // (beyond 448 s the answer is 448 whatever the quotient: the bound keeps it finite)
+          const float top = plain ? 512.0f * s[k] : INFINITY;
+          const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xffff0000u);
+          q[e] = e4m3x2(divide(fabsf(lo) > top ? copysignf(top, lo) : lo, s[k], r, plain),
+                        divide(fabsf(hi) > top ? copysignf(top, hi) : hi, s[k], r, plain));
+        }
+        *reinterpret_cast<uint2*>(dst + h * p.c.head_stride + c * 8) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+      } else {
+        *reinterpret_cast<uint4*>(dst + h * p.c.head_stride + c * 16) = x[k];
+      }
     }
   }
 }
@@ -102,12 +142,18 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // before them the budget - recent with the largest weights (equal weights: the
 // lowest position; NaN counts as less than every number), kept in their order.
 // Selection runs on the weights' bits mapped so that unsigned order is the
-// order of the numbers: four passes of an 8-bit histogram narrow down the
-// smallest key that stays and how many of its equals do, and two more passes
-// count and place what stays.  One CTA per (sequence, head); the passes after
-// the first find the keys in shared memory when they fit.
+// order of the numbers: histograms of 11, 11 and 10 bits narrow down the
+// smallest key that stays and how many of its equals do (one histogram is
+// enough where all of its last bin stay), and two more passes count and place
+// what stays.  One CTA per (sequence, head); the passes after the first find the
+// keys in shared memory when they fit.  11 bits are a float's sign, exponent and
+// two bits of fraction: weights spread over a few powers of two share no bin
+// with most lanes of a warp, and its additions go to shared memory one by one
+// without waiting for each other (8 bits at a time needed the lanes of equal
+// digit matched first: 38.7 us against 13 for 64 heads of 7000-8192 keys).
 constexpr int SEL_THREADS = 1024;
 constexpr int SEL_SMEM_KEYS = 48 * 1024;  // 192 KB
+constexpr int SEL_BINS = 2048;
 
 struct EvictParams {
   Cache c;         // source rows
@@ -123,6 +169,7 @@ struct EvictParams {
   int* lens_out;      // [B]
   int B, Hkv, budget, recent, max_out;
   int chunks;         // blocks of the move kernel for one (sequence, head)
+  Divider page;
   uint32_t* status;
 };
 
@@ -135,12 +182,10 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 
 __global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParams p) {
   extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[256];
+  __shared__ uint32_t hist[SEL_BINS];
   __shared__ int above_w[32], tie_w[32];
-  __shared__ uint32_t sh_prefix;
-  __shared__ int sh_need;
-  pdl_wait();
-  pdl_next();
+  __shared__ uint32_t sh_digit;
+  __shared__ int sh_need, sh_count;
   const int bh = blockIdx.x, b = bh / p.Hkv, h = bh % p.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = clamp_len(p.c, __ldg(p.lens + b));
@@ -158,62 +203,85 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParam
   const float* w = p.W + b * p.w_batch + h * p.w_head;
   const bool cached = old <= SEL_SMEM_KEYS;
   auto key_at = [&](int i) { return cached ? keys[i] : order_key(__ldg(w + i)); };
-  if (cached)
-    for (int i = tid; i < old; i += SEL_THREADS) keys[i] = order_key(__ldg(w + i));
-  // the pick-th largest key, eight bits at a time
-  uint32_t prefix = 0;
-  int need = pick;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0u;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int i0 = warp * 32; i0 < old; i0 += SEL_THREADS) {
-      const int i = i0 + lane;
-      const uint32_t k = i < old ? key_at(i) : 0u;
-      const bool in = i < old && (k & mask) == prefix;
-      const uint32_t digit = (k >> shift) & 255u;
-      // one addition for all lanes of equal digit
-      const unsigned peers = __match_any_sync(0xffffffffu, in ? digit : 256u + lane);
-      if (in && lane == __ffs(peers) - 1) atomicAdd(&hist[digit], (uint32_t)__popc(peers));
+  hist[tid] = hist[tid + SEL_THREADS] = 0u;
+  __syncthreads();
+  auto count = [&](uint32_t digit, bool in) {
+    // one addition for a warp of one digit, else one a lane
+    const unsigned who = __ballot_sync(0xffffffffu, in);
+    if (who == 0) return;
+    const uint32_t first = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
+    if (__all_sync(0xffffffffu, !in || digit == first)) {
+      if (lane == 0) atomicAdd(&hist[first], (uint32_t)__popc(who));
+    } else if (in) {
+      atomicAdd(&hist[digit], 1u);
     }
-    __syncthreads();
-    if (warp == 0) {
-      // lane L holds the digits 255 - 8L .. 248 - 8L, so that lanes go down
-      uint32_t c[8], sum = 0;
+  };
+  // the pick-th largest key: its upper bits `digits`, and how many of the keys
+  // that share these stay
+  uint32_t digits = 0;
+  int need = pick, shift = 21;
+  for (;;) {
+    if (shift == 21) {
+      constexpr int U = 4;  // loads in flight
+      for (int i0 = warp * 32; i0 < old; i0 += SEL_THREADS * U) {
+        float v[U];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += c[e] = hist[255 - 8 * lane - e];
-      uint32_t before = sum;
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * SEL_THREADS + lane;
+          v[u] = i < old ? __ldg(w + i) : 0.0f;
+        }
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
-      }
-      before -= sum;
-      if (before < (uint32_t)need && before + sum >= (uint32_t)need) {  // one lane
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (before < (uint32_t)need && before + c[e] >= (uint32_t)need) {
-            sh_prefix = prefix | ((uint32_t)(255 - 8 * lane - e) << shift);
-            sh_need = need - (int)before;
-            break;
-          }
-          before += c[e];
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * SEL_THREADS + lane;
+          const uint32_t k = order_key(v[u]);
+          if (cached && i < old) keys[i] = k;
+          count(k >> 21, i < old);
         }
       }
+    } else {
+      const int up = shift == 10 ? 21 : 10;  // bits already known
+      for (int i0 = warp * 32; i0 < old; i0 += SEL_THREADS) {
+        const int i = i0 + lane;
+        const uint32_t k = i < old ? key_at(i) : 0u;
+        count(shift == 10 ? (k >> 10) & 2047u : k & 1023u, i < old && (k >> up) == digits);
+      }
     }
     __syncthreads();
-    prefix = sh_prefix;
+    // thread T has the bins 2047 - 2 T and 2046 - 2 T, so that threads go down
+    const int top = SEL_BINS - 1 - 2 * tid;
+    const uint32_t c0 = hist[top], c1 = hist[top - 1];
+    uint32_t before = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    if (lane == 31) above_w[warp] = (int)before;
+    before -= c0 + c1;
+    __syncthreads();
+    hist[top] = hist[top - 1] = 0u;  // for the next digits
+    for (int v = 0; v < warp; ++v) before += (uint32_t)above_w[v];
+    if (before < (uint32_t)need && before + c0 + c1 >= (uint32_t)need) {  // one thread
+      const bool second = before + c0 < (uint32_t)need;
+      sh_digit = (uint32_t)(second ? top - 1 : top);
+      sh_need = need - (int)(second ? before + c0 : before);
+      sh_count = (int)(second ? c1 : c0);
+    }
+    __syncthreads();
+    digits = shift == 21 ? sh_digit : shift == 10 ? (digits << 11) | sh_digit : (digits << 10) | sh_digit;
     need = sh_need;
+    if (shift == 0 || need == sh_count) break;
+    shift = shift == 21 ? 10 : 0;
   }
-  // Keys above `prefix` stay, and the first `need` that equal it.  Each warp
+  // Keys above `digits` stay, and the first `need` that share them.  Each warp
   // takes a stretch of positions, counts, and then places.
   const int per = ((old + 31) / 32 + 31) / 32 * 32;
   const int i0 = min(old, warp * per), i1 = min(old, i0 + per);
   int above = 0, ties = 0;
   for (int i = i0 + lane; i - lane < i1; i += 32) {
-    const uint32_t k = i < i1 ? key_at(i) : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, i < i1 && k > prefix));
-    ties += __popc(__ballot_sync(0xffffffffu, i < i1 && k == prefix));
+    const uint32_t k = i < i1 ? key_at(i) >> shift : 0u;
+    above += __popc(__ballot_sync(0xffffffffu, i < i1 && k > digits));
+    ties += __popc(__ballot_sync(0xffffffffu, i < i1 && k == digits));
   }
   if (lane == 0) {
     above_w[warp] = above;
@@ -228,9 +296,9 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParam
   at += min(tie_at, need);
   const unsigned before_me = (1u << lane) - 1u;
   for (int i = i0 + lane; i - lane < i1; i += 32) {
-    const uint32_t k = i < i1 ? key_at(i) : 0u;
-    const unsigned tie = __ballot_sync(0xffffffffu, i < i1 && k == prefix);
-    const bool stays = i < i1 && (k > prefix || (k == prefix && tie_at + __popc(tie & before_me) < need));
+    const uint32_t k = i < i1 ? key_at(i) >> shift : 0u;
+    const unsigned tie = __ballot_sync(0xffffffffu, i < i1 && k == digits);
+    const bool stays = i < i1 && (k > digits || (k == digits && tie_at + __popc(tie & before_me) < need));
     const unsigned keep = __ballot_sync(0xffffffffu, stays);
     if (stays) kept[at + __popc(keep & before_me)] = i;
     at += __popc(keep);
@@ -246,8 +314,6 @@ constexpr int MOVE_ROWS = 4;
 
 template <int ROWB>
 __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const EvictParams p) {
-  pdl_wait();
-  pdl_next();
   constexpr int LPR = ROWB / 16, GROUPS = MOVE_THREADS / LPR, PER = GROUPS * MOVE_ROWS;
   const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const int b = bh / p.Hkv, h = bh % p.Hkv;
@@ -262,11 +328,12 @@ __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const EvictParams p)
     const int r = r0 + i * GROUPS + sub;
     dst[i] = -1;
     if (r < left) {
-      const int pos = __ldg(kept + r);
-      const long long src = row_offset(p.c, page_of(p.c, b, pos), pos % p.c.page_size);
-      const int slot = r / p.c.page_size;
-      const int page = slot < p.max_out ? __ldg(p.table_out + b * p.table_out_stride + slot) : -1;
-      dst[i] = row_offset(p.c, page, r % p.c.page_size);
+      // (pos < max_pages * page_size; rows past the destination table were refused)
+      const int pos = __ldg(kept + r), from = p.page(pos), to = p.page(r);
+      const int page = to < p.max_out ? __ldg(p.table_out + b * p.table_out_stride + to) : -1;
+      const long long src =
+          row_offset(p.c, __ldg(p.c.table + b * p.c.table_stride + from), pos - from * p.c.page_size);
+      dst[i] = row_offset(p.c, page, r - to * p.c.page_size);
       if (src < 0 || dst[i] < 0) {
         bad_page(p.status);
         dst[i] = -1;
@@ -312,13 +379,14 @@ fa_status launch_paged_append(const PagedCache& c, const Rows& K, const Rows& V,
   p.B = c.B;
   p.T = T;
   p.Hkv = c.Hkv;
+  p.page = paged::make_divider(c.page_size);
   p.status = st;
   constexpr int WARPS = paged::APPEND_THREADS / 32;
   const unsigned grid = (unsigned)((2LL * T + WARPS - 1) / WARPS);
   const bool e4m3 = c.elem == 1;
   auto* kern = c.d == 64 ? (e4m3 ? paged::append_kernel<64, true> : paged::append_kernel<64, false>)
                          : (e4m3 ? paged::append_kernel<128, true> : paged::append_kernel<128, false>);
-  return launch_early(kern, grid, paged::APPEND_THREADS, 0, s, p) ? FA_OK : FA_ERR_CUDA;
+  return launch(kern, grid, paged::APPEND_THREADS, 0, s, p) ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status launch_paged_evict(const PagedCache& c, const Evict& e, cudaStream_t s) {
@@ -343,19 +411,20 @@ fa_status launch_paged_evict(const PagedCache& c, const Evict& e, cudaStream_t s
   p.budget = e.budget;
   p.recent = e.recent;
   p.max_out = e.max_out;
+  p.page = paged::make_divider(c.page_size);
   p.status = st;
   // shared memory for the keys a head can have to choose from, when they fit
   const long long most = (long long)c.max_pages * c.page_size - e.recent;
   const int smem = 4 * (int)(most < 0 ? 0 : most < paged::SEL_SMEM_KEYS ? most : paged::SEL_SMEM_KEYS);
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(done, (const void*)paged::select_kernel, 4 * paged::SEL_SMEM_KEYS) ||
-      !launch_early(paged::select_kernel, (unsigned)(c.B * c.Hkv), paged::SEL_THREADS, smem, s, p))
+      !launch(paged::select_kernel, (unsigned)(c.B * c.Hkv), paged::SEL_THREADS, smem, s, p))
     return FA_ERR_CUDA;
   bool ok;
   auto move = [&](auto kern, int rowb) {
     const int per = paged::MOVE_THREADS / (rowb / 16) * paged::MOVE_ROWS;
     p.chunks = (e.budget + per - 1) / per;
-    ok = launch_early(kern, (unsigned)(c.B * c.Hkv * p.chunks), paged::MOVE_THREADS, 0, s, p);
+    ok = launch(kern, (unsigned)(c.B * c.Hkv * p.chunks), paged::MOVE_THREADS, 0, s, p);
   };
   const int rowb = c.d * c.elem;
   if (rowb == 64) move(paged::move_kernel<64>, 64);

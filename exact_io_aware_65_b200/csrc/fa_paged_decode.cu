@@ -159,8 +159,6 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
   __shared__ int start_b;
   __shared__ long long sh_total;
 
-  pdl_wait();
-  pdl_next();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int HU = p.Hkv * p.HB, cta = blockIdx.x;
@@ -592,8 +590,6 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
 // Block (c, r): row r of the unit that begins in CTA c and ends in another.
 template <int D>
 __global__ void __launch_bounds__(D) join_kernel(const DecodeParams p, int rows) {
-  pdl_wait();
-  pdl_next();
   const int c0 = blockIdx.x / rows, r = blockIdx.x % rows, col = threadIdx.x;
   const int4 u = p.desc[c0];
   if (u.x < 0) return;
@@ -623,8 +619,6 @@ __global__ void __launch_bounds__(D) join_kernel(const DecodeParams p, int rows)
 constexpr int W_THREADS = 256;
 __global__ void __launch_bounds__(W_THREADS) weights_kernel(const DecodeParams p, float* A, long long a_batch,
                                                             long long a_head, int accumulate, int chunks) {
-  pdl_wait();
-  pdl_next();
   const int bh = blockIdx.x / chunks, b = bh / p.Hkv, hk = bh % p.Hkv;
   const int len = clamp_len(p.c, __ldg(p.lens + b));
   const long long first = (long long)b * p.Hq + hk * p.G;
@@ -692,13 +686,13 @@ static fa_status launch_d(paged::DecodeParams p, int B, const PagedDecode& a, in
     p.O = O + (long long)b0 * p.Hq * D;
     p.LSE = LSE + (long long)b0 * p.Hq;
     if (scores) p.scores = scores + (long long)b0 * p.Hq * p.pitch;
-    if (!launch_early(kern, (unsigned)grid, THREADS, smem, s, p)) return FA_ERR_CUDA;
+    if (!launch(kern, (unsigned)grid, THREADS, smem, s, p)) return FA_ERR_CUDA;
     const int rows = p.G < p.R ? p.G : p.R;
-    if (!launch_early(join_kernel<D>, (unsigned)(grid * rows), D, 0, s, p, rows)) return FA_ERR_CUDA;
+    if (!launch(join_kernel<D>, (unsigned)(grid * rows), D, 0, s, p, rows)) return FA_ERR_CUDA;
     if (scores) {
       long long chunks = (p.pitch + 4 * W_THREADS - 1) / (4 * W_THREADS);  // four keys a thread
       if (chunks > 64) chunks = 64;
-      if (!launch_early(weights_kernel, (unsigned)(p.B * p.Hkv * chunks), W_THREADS, 0, s, p, a.W + b0 * a.w_batch,
+      if (!launch(weights_kernel, (unsigned)(p.B * p.Hkv * chunks), W_THREADS, 0, s, p, a.W + b0 * a.w_batch,
                         a.w_batch, a.w_head, a.accumulate, (int)chunks))
         return FA_ERR_CUDA;
     }
@@ -735,13 +729,13 @@ fa_status launch_paged_decode(const PagedCache& c, const PagedDecode& a, cudaStr
   p.O = static_cast<__nv_bfloat16*>(a.O);
   p.LSE = a.LSE;
   p.status = st;
-  auto launch = [&](auto nb) {
+  auto run = [&](auto nb) {
     constexpr int NB = decltype(nb)::value;
     if (c.elem == 1)
       return c.d == 64 ? launch_d<64, true, NB>(p, c.B, a, grid, s) : launch_d<128, true, NB>(p, c.B, a, grid, s);
     return c.d == 64 ? launch_d<64, false, NB>(p, c.B, a, grid, s) : launch_d<128, false, NB>(p, c.B, a, grid, s);
   };
-  return p.R == 8 ? launch(std::integral_constant<int, 1>()) : launch(std::integral_constant<int, 2>());
+  return p.R == 8 ? run(std::integral_constant<int, 1>()) : run(std::integral_constant<int, 2>());
 }
 
 }  // namespace fa

@@ -381,12 +381,6 @@ __device__ __forceinline__ void regs_inc() {
   if constexpr (N != 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Wait until the kernels before this one in the stream have completed and their
-// writes can be seen (nothing to wait for unless launched by launch_early).
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// The next kernel in the stream may be set up from here on.
-__device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 __device__ __forceinline__ int warp_id() { return threadIdx.x >> 5; }
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 31; }
 

@@ -276,7 +276,7 @@ typedef struct {
  *      cu_seqlens[b] <= t < cu_seqlens[b+1] (DEVICE int [B+1], ascending) and
  *      goes to position lens[b] + t - cu_seqlens[b] (lens: DEVICE int [B], the
  *      positions already held; the call does not change it).  Rows that
- *      belong to no sequence are not read.  T = 0 does nothing.
+ *      belong to no sequence go nowhere.  T = 0 does nothing.
  * Out: the pools' rows: a copy (FA_CACHE_BF16), or x / scale rounded to the
  *      nearest 8-bit value, ties to even, magnitudes above 448 held at 448.
  * Two rows that go to one slot (a page listed twice) leave either of them. */
