@@ -359,10 +359,14 @@ def _run(name, device, stream, *args):
         raise FAError(code, name)
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, device, stream, like=None):
     """A new buffer for a call on ``stream``: the allocator hands memory out in
-    the order of the stream it is asked on, so that must be the call's."""
+    the order of the stream it is asked on, so that must be the call's.
+    ``like``: a tensor that has the shape and type, if it happens to be
+    contiguous (a cheaper call)."""
     if stream is None:
+        if like is not None and like.is_contiguous():
+            return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
@@ -376,20 +380,24 @@ _BF16, _E4M3 = torch.bfloat16, torch.float8_e4m3fn
 def _rows(t, name, heads=None, d=None, rows=None, device=None):
     """fa_rows of a bf16 CUDA tensor [rows, heads, d] whose last dimension is
     contiguous; the rows and heads may be strided."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is _BF16 and t.dim() == 3):
+    try:
+        n, h, w = t.shape
+        rs, hs, ds = t.stride()
+        ptr = t.data_ptr()
+        good = t.dtype is _BF16 and t.is_cuda
+    except (AttributeError, ValueError, TypeError, RuntimeError):
+        good = False
+    if not good:
         raise FAError(1, f"{name} must be a bf16 CUDA tensor [rows, heads, d]")
-    n, h, w = t.shape
     if (heads is not None and h != heads) or (d is not None and w != d) or (rows is not None and n != rows):
         raise FAError(1, f"{name} must be [{'rows' if rows is None else rows}, {'heads' if heads is None else heads}, "
                          f"{'d' if d is None else d}], got {tuple(t.shape)}")
     if device is not None and t.device != device:
         raise FAError(1, f"{name} must be on {device}, got {t.device}")
-    rs, hs, ds = t.stride()
     if n <= 1:  # the stride of a single row or head is never used
         rs = h * w
     if h <= 1:
         hs = w
-    ptr = t.data_ptr()
     if (ds != 1 and w > 1) or (rs | hs) & 7 or ptr & 15:
         raise FAError(1, f"{name}: d must be contiguous, and rows and heads start on 16-byte boundaries (strides "
                          f"{t.stride()})")
@@ -398,8 +406,8 @@ def _rows(t, name, heads=None, d=None, rows=None, device=None):
 
 def _int32(t, name, n, device):
     """Device pointer of a contiguous int32 vector [n]."""
-    if not (isinstance(t, torch.Tensor) and t.device == device and t.dtype == torch.int32 and t.dim() == 1
-            and t.is_contiguous() and t.shape[0] == n):
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == (n,) and t.device == device
+            and t.is_contiguous()):
         raise FAError(1, f"{name} must be a contiguous int32 tensor [{n}] on {device}")
     return t.data_ptr()
 
@@ -446,7 +454,7 @@ def fwd_packed(Q, K, V, cu_q, cu_k, mask="none", scale=None, O=None, LSE=None, w
     B = _sequences(cu_q)
     scale = d ** -0.5 if scale is None else float(scale)
     if O is None:
-        O = _empty((Tq, Hq, d), torch.bfloat16, dev, stream)
+        O = _empty((Tq, Hq, d), _BF16, dev, stream, Q)
     o = _rows(O, "O", Hq, d, Tq, dev)
     LSE = _empty((Hq, Tq), torch.float32, dev, stream) if LSE is None else \
         _check_buf(LSE, "LSE", (Hq, Tq), torch.float32, dev)
@@ -479,8 +487,12 @@ def bwd_packed(Q, K, V, O, dO, LSE, cu_q, cu_k, mask="none", scale=None, dQ=None
     _check_buf(LSE, "LSE", (Hq, Tq), torch.float32, dev)
     B = _sequences(cu_q)
     scale = d ** -0.5 if scale is None else float(scale)
-    dQ, dK, dV = (_empty((T, H, d), torch.bfloat16, dev, stream) if t is None else t
-                  for t, T, H in ((dQ, Tq, Hq), (dK, Tk, Hkv), (dV, Tk, Hkv)))
+    if dQ is None:
+        dQ = _empty((Tq, Hq, d), _BF16, dev, stream, Q)
+    if dK is None:
+        dK = _empty((Tk, Hkv, d), _BF16, dev, stream, K)
+    if dV is None:
+        dV = _empty((Tk, Hkv, d), _BF16, dev, stream, V)
     dq, dk, dv = _rows(dQ, "dQ", Hq, d, Tq, dev), _rows(dK, "dK", Hkv, d, Tk, dev), _rows(dV, "dV", Hkv, d, Tk, dev)
     need = bwd_packed_workspace_size(B, Tq, Tk, Hq, Hkv, d)
     if workspace is None:
@@ -568,8 +580,7 @@ def paged_decode(Q, k_cache, v_cache, page_table, lens, scale=None, k_scale=None
     wp = wb = wh = 0
     if weights is not None:
         wp, wb, wh = _weights(weights, "weights", B, c.Hkv, cap, dev)
-    O = _empty((B, Hq, d), torch.bfloat16, dev, stream) if O is None else \
-        _check_buf(O, "O", (B, Hq, d), torch.bfloat16, dev)
+    O = _empty((B, Hq, d), _BF16, dev, stream, Q) if O is None else _check_buf(O, "O", (B, Hq, d), _BF16, dev)
     LSE = _empty((B, Hq), torch.float32, dev, stream) if LSE is None else \
         _check_buf(LSE, "LSE", (B, Hq), torch.float32, dev)
     need = paged_decode_workspace_size(B, Hq, c.Hkv, d, cap, weights is not None)

@@ -17,17 +17,15 @@ namespace fa {
 __device__ uint32_t g_status = 0;
 
 uint32_t* status_word() {
-  static uint32_t* addr[64] = {};
-  static std::mutex mu;
+  static std::atomic<uint32_t*> addr[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-  std::lock_guard<std::mutex> lock(mu);
-  if (!addr[dev]) {
-    void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) return nullptr;
-    addr[dev] = static_cast<uint32_t*>(p);
-  }
-  return addr[dev];
+  uint32_t* known = addr[dev].load(std::memory_order_acquire);
+  if (known) return known;
+  void* p = nullptr;  // (two threads may both look it up: they find the same)
+  if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) return nullptr;
+  addr[dev].store(static_cast<uint32_t*>(p), std::memory_order_release);
+  return static_cast<uint32_t*>(p);
 }
 
 static std::atomic<uint64_t> g_wait_timeout_ns{4000000000ull};
@@ -43,9 +41,12 @@ bool allow_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes) {
 }
 
 int num_sms() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
