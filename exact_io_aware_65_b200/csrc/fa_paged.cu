@@ -57,15 +57,42 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-// x / s from r, the correctly rounded 1 / s: with the exact remainder of the
-// first quotient, the second is x / s correctly rounded (Markstein's theorem,
-// "Computation of elementary functions on the IBM RISC System/6000", 1990).  It
-// holds while nothing on the way under- or overflows; `plain` scales are those
-// for which no bf16 x that is not held at 448 anyway, nor rounded to zero, can.
-__device__ __forceinline__ float divide(float x, float s, float r, bool plain) {
-  if (!plain) return __fdiv_rn(x, s);
+// Keeps x within +-top; NaN stays.
+__device__ __forceinline__ float hold(float x, float top) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(top));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(-top));
+  return r;
+}
+
+// x / s from r, the correctly rounded 1 / s: with the remainder of the first
+// quotient, the second is x / s correctly rounded but for rare last bits
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000",
+// 1990, proves it for a first quotient within a unit of its last place; where it
+// is exact, as on the borders between 8-bit values, so is the second).  For
+// scales between 2^-60 and 2^60 and |x| <= 512 s nothing overflows on the way,
+// and what underflows rounds to zero in 8 bits anyway.
+__device__ __forceinline__ float divide(float x, float s, float r) {
   const float q = __fmul_rn(x, r);
   return q == 0.0f ? q : __fmaf_rn(__fmaf_rn(-q, s, x), r, q);  // (a zero keeps its sign)
+}
+
+// Eight bf16 to eight 8-bit values of x / s.
+__device__ __forceinline__ uint2 encode(const uint4& x, float s) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t q[4];
+  if (s > 0x1p-60f && s < 0x1p60f) {
+    const float r = __frcp_rn(s), top = 512.0f * s;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      q[e] = e4m3x2(divide(hold(__uint_as_float(w[e] << 16), top), s, r),
+                    divide(hold(__uint_as_float(w[e] & 0xffff0000u), top), s, r));
+  } else {
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e)
+      q[e] = e4m3x2(__fdiv_rn(__uint_as_float(w[e] << 16), s), __fdiv_rn(__uint_as_float(w[e] & 0xffff0000u), s));
+  }
+  return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
 }
 
 // A warp per (token, K or V): 16 bytes of the input a lane, four pieces of it in
@@ -117,19 +144,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
       const int i = i0 + 32 * k, h = i / CH, c = i % CH;
       if (i >= pieces) break;
       if (E4M3) {
-        const bool plain = s[k] > 0x1p-60f && s[k] < 0x1p60f;
-        const float r = __frcp_rn(s[k]);
-        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-        uint32_t q[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // (beyond 448 s the answer is 448 whatever the quotient: the bound keeps it finite)
-          const float top = plain ? 512.0f * s[k] : INFINITY;
-          const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xffff0000u);
-          q[e] = e4m3x2(divide(fabsf(lo) > top ? copysignf(top, lo) : lo, s[k], r, plain),
-                        divide(fabsf(hi) > top ? copysignf(top, hi) : hi, s[k], r, plain));
-        }
-        *reinterpret_cast<uint2*>(dst + h * p.c.head_stride + c * 8) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+        *reinterpret_cast<uint2*>(dst + h * p.c.head_stride + c * 8) = encode(x[k], s[k]);
       } else {
         *reinterpret_cast<uint4*>(dst + h * p.c.head_stride + c * 16) = x[k];
       }

@@ -138,7 +138,9 @@ struct DCfg {
   static constexpr int JPITCH = D + 4;
   static constexpr int JOIN_BYTES = WARPS * R * JPITCH * 4 > MAX_BATCH * 4 ? WARPS * R * JPITCH * 4 : MAX_BATCH * 4;
   static constexpr int FIT = (224 * 1024 - R * QPITCH - JOIN_BYTES) / (WARPS * UNIT);
-  static constexpr int NU = FIT < 8 ? FIT : 8;  // units of a ring
+  // Units of a ring: an odd number, so that a step frees the places of the K and
+  // V of one later step, whose rows are looked up once.
+  static constexpr int NU = FIT < 7 ? (FIT - 1) / 2 * 2 + 1 : 7;
   static_assert(NU >= 3, "shared memory");
   static constexpr int SMEM_BYTES = WARPS * NU * UNIT + R * QPITCH + JOIN_BYTES;
 };
@@ -149,7 +151,6 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
   constexpr int ROWB = C::ROWB, R = C::R, NU = C::NU;
   constexpr int PIECES = ROWB / 16;
   constexpr int RPI = 32 / PIECES;  // rows a warp copies per instruction
-  constexpr int AHEAD = NU - 1;     // units copied ahead
   constexpr int KS = D / 16;        // 16-column steps of a row
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* sQ = smem + WARPS * NU * C::UNIT;
@@ -210,8 +211,9 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
   __syncthreads();  // prefix has been read
   if (w.at >= w.end) return;
 
-  // ---- the copies run AHEAD units ahead of the products, the page lookups a
-  // step ahead of the copies.  Lane r (and r + 16) looks up row r of a step.
+  // ---- the copies run up to NU units ahead of the products (K, V, K, V, ...),
+  // the page lookups a step ahead of the copies.  Lane r (and r + 16) looks up
+  // row r of a step.
   const uint32_t ring = smem_u32(smem) + warp * (NU * C::UNIT);
   const int piece = lane % PIECES, row_of_lane = lane / PIECES;
   Walk f = w;  // the next step to look up
@@ -251,35 +253,41 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
     real = __ballot_sync(0xffffffffu, good);
     head_off = page_hk * p.c.head_stride + piece * 16;
   };
+  auto after = [](uint32_t slot) { return slot + 1 == NU ? 0u : slot + 1; };
   uint32_t put = 0;  // ring slot of the next unit
-  auto copy_unit = [&](const uint8_t* pool) {
-    const uint32_t dst = ring + put * C::UNIT;
-    put = put + 1 == NU ? 0 : put + 1;
-    const uint8_t* src = pool + head_off;
+  // K, V or both of the step at hand, a group each; after its V the next step
+  // is at hand.
+  auto copy_rows = [&](bool k, bool v) {
+    uint32_t lo[STEP / RPI], hi[STEP / RPI];
 #pragma unroll
     for (int i = 0; i < STEP / RPI; ++i) {
-      const int r = i * RPI + row_of_lane;
-      unsigned long long off = __shfl_sync(0xffffffffu, off_lo, r);
-      if (p.wide) off |= (unsigned long long)__shfl_sync(0xffffffffu, off_hi, r) << 32;
-      const bool read = (real >> r) & 1u;
-      cp16(dst + piece_at<ROWB>(r, piece), src + (off << 4), read);
+      lo[i] = __shfl_sync(0xffffffffu, off_lo, i * RPI + row_of_lane);
+      hi[i] = p.wide ? __shfl_sync(0xffffffffu, off_hi, i * RPI + row_of_lane) : 0u;
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  auto copy_k = [&]() { copy_unit(p.c.K); };
-  auto copy_v = [&]() {
-    copy_unit(p.c.V);
-    next_rows();
-    look_up();
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      if (kv == 0 ? !k : !v) continue;
+      const uint32_t dst = ring + put * C::UNIT;
+      const uint8_t* src = (kv == 0 ? p.c.K : p.c.V) + head_off;
+#pragma unroll
+      for (int i = 0; i < STEP / RPI; ++i) {
+        const int r = i * RPI + row_of_lane;
+        const unsigned long long off = ((unsigned long long)hi[i] << 32 | lo[i]) << 4;
+        cp16(dst + piece_at<ROWB>(r, piece), src + off, (real >> r) & 1u);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      put = after(put);
+    }
+    if (v) {
+      next_rows();
+      look_up();
+    }
   };
   look_up();
   next_rows();
   look_up();
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) {
-    if (i & 1) copy_v();
-    else copy_k();
-  }
+  for (int i = 0; i < NU; i += 2) copy_rows(true, i + 1 < NU);
 
   uint32_t got = 0;  // ring slot of the next unit to use
   while (w.at < w.end) {
@@ -364,148 +372,183 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
       l[n][0] = l[n][1] = 0.0f;
     }
 
-    for (int step = 0; step < nseg; ++step) {
+    // Products of 32 columns (i, i + 1 of the 16-column steps).  S^T += K Q^T, two
+    // chains of products:
+    float c[NB][2][4];
+    const int mi = lane >> 3, lr = lane & 7;  // ldmatrix: matrix and row of this lane's address
+    auto clear = [&]() {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[n][0][e] = c[n][1][e] = 0.0f;
+    };
+    auto mul_k = [&](uint32_t sK, int s) {
+      uint32_t q4[NB][4];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        if (NB == 1) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q4[n][e] = qb[NB == 1 ? s / 2 : 0][e];
+        } else {
+          ldsm4(q4[n], q_at + n * 8 * C::QPITCH + s * 32);
+        }
+      }
+      const int kr = (mi & 1) * 8 + lr;
+      uint32_t a0[4], a1[4];
+      if (E4M3) {  // a piece is 16 columns
+        uint32_t r[4];
+        ldsm4(r, sK + piece_at<ROWB>(kr, s + (mi >> 1)));
+        a0[0] = widen(r[0]);
+        a0[1] = widen(r[1]);
+        a0[2] = widen(r[0] >> 16);
+        a0[3] = widen(r[1] >> 16);
+        a1[0] = widen(r[2]);
+        a1[1] = widen(r[3]);
+        a1[2] = widen(r[2] >> 16);
+        a1[3] = widen(r[3] >> 16);
+      } else {
+        ldsm4(a0, sK + piece_at<ROWB>(kr, 2 * s + (mi >> 1)));
+        ldsm4(a1, sK + piece_at<ROWB>(kr, 2 * s + 2 + (mi >> 1)));
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        mma<E4M3>(c[n][0], a0, q4[n][0], q4[n][1]);
+        mma<E4M3>(c[n][1], a1, q4[n][2], q4[n][3]);
+      }
+    };
+    // O^T += V^T P^T (ldmatrix transposed):
+    uint32_t pb[NB][2];  // P^T as B operand
+    auto mul_v = [&](uint32_t sV, int i) {
+      uint32_t a0[4], a1[4];
+      if (E4M3) {
+        // bytes (key, col), (key, col + 1), (key + 1, col), (key + 1, col + 1): the
+        // even columns are rows g of the tile, the odd ones rows g + 8
+        uint32_t r[4];
+        ldsm4_t(r, sV + piece_at<ROWB>((mi & 1) * 8 + lr, i + (mi >> 1)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = __byte_perm(r[e], 0, 0x3120);
+        a0[0] = widen(r[0]);
+        a0[1] = widen(r[0] >> 16);
+        a0[2] = widen(r[1]);
+        a0[3] = widen(r[1] >> 16);
+        a1[0] = widen(r[2]);
+        a1[1] = widen(r[2] >> 16);
+        a1[2] = widen(r[3]);
+        a1[3] = widen(r[3] >> 16);
+      } else {
+        const int kr = (mi >> 1) * 8 + lr;
+        ldsm4_t(a0, sV + piece_at<ROWB>(kr, 2 * i + (mi & 1)));
+        ldsm4_t(a1, sV + piece_at<ROWB>(kr, 2 * i + 2 + (mi & 1)));
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        mma<E4M3>(o[i][n], a0, pb[n][0], pb[n][1]);
+        mma<E4M3>(o[i + 1][n], a1, pb[n][0], pb[n][1]);
+      }
+    };
+    // Online softmax of step `step`'s scores; a lane has keys g, g + 8 of heads 2 t, 2 t + 1.
+    auto softmax = [&](int step) {
       const int key0 = (w.blk + step) * BLOCK + warp * STEP;
-      const int valid = w.len - key0;  // keys of this step that exist (may be <= 0)
-      asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
-      __syncwarp();
-      // the slot this unit goes to was read out in the step before
-      if (AHEAD & 1) copy_v();
-      else copy_k();
-      const uint32_t sK = ring + got * C::UNIT;
-      got = got + 1 == NU ? 0 : got + 1;
-      uint32_t pb[NB][2];  // P^T as B operand
-      if (valid > 0) {
-        // ---- S^T = K Q^T
-        float c[NB][2][4] = {};  // two chains of products
-        const int mi = lane >> 3, kr = (mi & 1) * 8 + (lane & 7);
+      const int valid = w.len - key0;  // keys of this step that exist (may be <= 0: then P = 0)
+      float x[NB][4];
+      bool above = false;
 #pragma unroll
-        for (int s = 0; s < KS; s += 2) {
-          uint32_t q4[NB][4];
+      for (int n = 0; n < NB; ++n) {
 #pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            if (NB == 1) {
+        for (int e = 0; e < 4; ++e)
+          x[n][e] = g + (e >> 1) * 8 < valid ? (c[n][0][e] + c[n][1][e]) * sl2[n][e & 1] : -INFINITY;
+        if (p.scores && valid > 0) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) q4[n][e] = qb[NB == 1 ? s / 2 : 0][e];
-            } else {
-              ldsm4(q4[n], q_at + n * 8 * C::QPITCH + s * 32);
+          for (int e = 0; e < 2; ++e) {
+            const int h = n * 8 + 2 * t + e;
+            if (h < heads) {
+              float* row = p.scores + (q_first + h) * p.pitch + key0 + g;
+              row[0] = x[n][e];
+              row[8] = x[n][e + 2];
             }
           }
-          uint32_t a0[4], a1[4];
-          if (E4M3) {  // a piece is 16 columns
-            uint32_t r[4];
-            ldsm4(r, sK + piece_at<ROWB>(kr, s + (mi >> 1)));
-            a0[0] = widen(r[0]);
-            a0[1] = widen(r[1]);
-            a0[2] = widen(r[0] >> 16);
-            a0[3] = widen(r[1] >> 16);
-            a1[0] = widen(r[2]);
-            a1[1] = widen(r[3]);
-            a1[2] = widen(r[2] >> 16);
-            a1[3] = widen(r[3] >> 16);
-          } else {
-            ldsm4(a0, sK + piece_at<ROWB>(kr, 2 * s + (mi >> 1)));
-            ldsm4(a1, sK + piece_at<ROWB>(kr, 2 * s + 2 + (mi >> 1)));
-          }
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            mma<E4M3>(c[n][0], a0, q4[n][0], q4[n][1]);
-            mma<E4M3>(c[n][1], a1, q4[n][2], q4[n][3]);
-          }
-        }
-        // ---- online softmax; a lane has keys g, g + 8 of heads 2 t, 2 t + 1
-        float x[NB][4];
-        bool above = false;
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[n][e] = g + (e >> 1) * 8 < valid ? (c[n][0][e] + c[n][1][e]) * sl2[n][e & 1] : -INFINITY;
-          if (p.scores) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int h = n * 8 + 2 * t + e;
-              if (h < heads) {
-                float* row = p.scores + (q_first + h) * p.pitch + key0 + g;
-                row[0] = x[n][e];
-                row[8] = x[n][e + 2];
-              }
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) above |= fmaxf(x[n][e], x[n][e + 2]) > m[n][e] + SLACK;
-        }
-        if (__any_sync(0xffffffffu, above)) {
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(x[n][e], x[n][e + 2]);
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              mx = fmaxf(mx, m[n][e]);
-              const float down = ex2_approx(m[n][e] - (mx == -INFINITY ? 0.0f : mx));
-              m[n][e] = mx;
-              l[n][e] *= down;
-#pragma unroll
-              for (int i = 0; i < KS; ++i) {
-                o[i][n][e] *= down;
-                o[i][n][e + 2] *= down;
-              }
-            }
         }
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          const float r0 = m[n][0] == -INFINITY ? 0.0f : m[n][0];  // every score so far -inf: P = 0
-          const float r1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
-          const float p0 = ex2_approx(x[n][0] - r0), p1 = ex2_approx(x[n][1] - r1);
-          const float p2 = ex2_approx(x[n][2] - r0), p3 = ex2_approx(x[n][3] - r1);
-          l[n][0] += p0 + p2;
-          l[n][1] += p1 + p3;
-          pb[n][0] = transpose8x8(pack2<E4M3>(p0, p1));
-          pb[n][1] = transpose8x8(pack2<E4M3>(p2, p3));
-        }
+        for (int e = 0; e < 2; ++e) above |= fmaxf(x[n][e], x[n][e + 2]) > m[n][e] + SLACK;
       }
-      asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
-      __syncwarp();
-      if (AHEAD & 1) copy_k();
-      else copy_v();
-      const uint32_t sV = ring + got * C::UNIT;
-      got = got + 1 == NU ? 0 : got + 1;
-      if (valid > 0) {
-        // ---- O^T += V^T P^T (ldmatrix transposed)
-        const int mi = lane >> 3;
+      if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-        for (int i = 0; i < KS; i += 2) {
-          uint32_t a0[4], a1[4];
-          if (E4M3) {
-            // bytes (key, col), (key, col + 1), (key + 1, col), (key + 1, col + 1): the
-            // even columns are rows g of the tile, the odd ones rows g + 8
-            uint32_t r[4];
-            ldsm4_t(r, sV + piece_at<ROWB>((mi & 1) * 8 + (lane & 7), i + (mi >> 1)));
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) r[e] = __byte_perm(r[e], 0, 0x3120);
-            a0[0] = widen(r[0]);
-            a0[1] = widen(r[0] >> 16);
-            a0[2] = widen(r[1]);
-            a0[3] = widen(r[1] >> 16);
-            a1[0] = widen(r[2]);
-            a1[1] = widen(r[2] >> 16);
-            a1[2] = widen(r[3]);
-            a1[3] = widen(r[3] >> 16);
-          } else {
-            const int kr = (mi >> 1) * 8 + (lane & 7);
-            ldsm4_t(a0, sV + piece_at<ROWB>(kr, 2 * i + (mi & 1)));
-            ldsm4_t(a1, sV + piece_at<ROWB>(kr, 2 * i + 2 + (mi & 1)));
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(x[n][e], x[n][e + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            mx = fmaxf(mx, m[n][e]);
+            const float down = ex2_approx(m[n][e] - (mx == -INFINITY ? 0.0f : mx));
+            m[n][e] = mx;
+            l[n][e] *= down;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              o[i][n][e] *= down;
+              o[i][n][e + 2] *= down;
+            }
           }
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            mma<E4M3>(o[i][n], a0, pb[n][0], pb[n][1]);
-            mma<E4M3>(o[i + 1][n], a1, pb[n][0], pb[n][1]);
-          }
-        }
       }
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const float r0 = m[n][0] == -INFINITY ? 0.0f : m[n][0];  // every score so far -inf: P = 0
+        const float r1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
+        const float p0 = ex2_approx(x[n][0] - r0), p1 = ex2_approx(x[n][1] - r1);
+        const float p2 = ex2_approx(x[n][2] - r0), p3 = ex2_approx(x[n][3] - r1);
+        l[n][0] += p0 + p2;
+        l[n][1] += p1 + p3;
+        pb[n][0] = transpose8x8(pack2<E4M3>(p0, p1));
+        pb[n][1] = transpose8x8(pack2<E4M3>(p2, p3));
+      }
+    };
+    // The place of the next unit to use.  At every wait below NU units behind the
+    // last used one are on their way, so that all but NU - 1 (or, where two are
+    // used, NU - 2) of them having landed means that it has; once used, a unit's
+    // place goes to the one NU later.
+    auto use = [&]() {
+      const uint32_t at = ring + got * C::UNIT;
+      got = after(got);
+      return at;
+    };
+
+    // S of the first step; then S of a step together with P V of the step before
+    // (independent products side by side: the two warps of a scheduler do not
+    // hide each other's latencies); at last P V of the last.
+    {
+      asm volatile("cp.async.wait_group %0;" ::"n"(NU - 1) : "memory");
+      __syncwarp();
+      const uint32_t sK = use();
+      clear();
+#pragma unroll
+      for (int i = 0; i < KS; i += 2) mul_k(sK, i);
+      __syncwarp();
+      copy_rows(false, true);
+      softmax(0);
+    }
+    for (int step = 1; step < nseg; ++step) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(NU - 2) : "memory");
+      __syncwarp();
+      const uint32_t sV = use(), sK = use();
+      clear();
+#pragma unroll
+      for (int i = 0; i < KS; i += 2) {
+        mul_k(sK, i);
+        mul_v(sV, i);
+      }
+      __syncwarp();
+      copy_rows(true, true);
+      softmax(step);
+    }
+    {
+      asm volatile("cp.async.wait_group %0;" ::"n"(NU - 1) : "memory");
+      __syncwarp();
+      const uint32_t sV = use();
+#pragma unroll
+      for (int i = 0; i < KS; i += 2) mul_v(sV, i);
+      __syncwarp();
+      copy_rows(true, false);
     }
 
     // ---- join the eight warps, in their order
@@ -596,19 +639,29 @@ __global__ void __launch_bounds__(D) join_kernel(const DecodeParams p, int rows)
   const int hk = u.y / p.HB, row0 = (u.y % p.HB) * p.R;
   if (r >= min(p.R, p.G - row0)) return;
   // in CTAs after c0 the unit comes first: slot 2 c
-  const int first = u.z;
+  auto part_row = [&](int i) { return (long long)(i ? 2 * (c0 + i) : u.z) * ROWS + r; };
+  // every warp finds the maximum and the sum, a part a lane; 2^(m - M) of the
+  // parts to shared memory
+  __shared__ float factor[1024];  // (a part a CTA, a CTA an SM)
+  const int lane = col & 31;
   float M = -INFINITY;
-  for (int i = 0; i < u.w; ++i) M = fmaxf(M, p.ml[(long long)(i ? 2 * (c0 + i) : first) * ROWS + r].x);
+  for (int i = lane; i < u.w; i += 32) M = fmaxf(M, p.ml[part_row(i)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float ref = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f, acc = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < u.w; ++i) {
-    const long long slot = (long long)(i ? 2 * (c0 + i) : first) * ROWS + r;
-    const float2 ml = p.ml[slot];
+  float L = 0.0f;
+  for (int i = lane; i < u.w; i += 32) {
+    const float2 ml = p.ml[part_row(i)];
     const float f = ex2_approx(ml.x - ref);
     L = fmaf(ml.y, f, L);
-    acc = fmaf(p.part[slot * D + col], f, acc);
+    if (col < 32) factor[i] = f;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  __syncthreads();
+  float acc = 0.0f;
+#pragma unroll 8
+  for (int i = 0; i < u.w; ++i) acc = fmaf(p.part[part_row(i) * D + col], factor[i], acc);
   const long long row = (long long)u.x * p.Hq + hk * p.G + row0 + r;
   p.O[row * D + col] = __float2bfloat16(L == 0.0f ? 0.0f : acc / L);
   if (col == 0) p.LSE[row] = (M + log2f(L)) * LN2;
@@ -643,6 +696,9 @@ __global__ void __launch_bounds__(W_THREADS) weights_kernel(const DecodeParams p
   }
 }
 
+// One CTA per SM, at most as many as the join kernel keeps factors for.
+static int decode_grid() { return num_sms() < 1024 ? num_sms() : 1024; }
+
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct DecodeLayout {
@@ -661,7 +717,7 @@ static DecodeLayout layout(int B, int Hq, int d, long long cap, bool weights, in
 }  // namespace paged
 
 size_t paged_decode_workspace_bytes(int B, int Hq, int d, long long cap, bool weights) {
-  return paged::layout(B, Hq, d, cap, weights, num_sms()).total;
+  return paged::layout(B, Hq, d, cap, weights, paged::decode_grid()).total;
 }
 
 template <int D, bool E4M3, int NB>
@@ -703,7 +759,7 @@ static fa_status launch_d(paged::DecodeParams p, int B, const PagedDecode& a, in
 fa_status launch_paged_decode(const PagedCache& c, const PagedDecode& a, cudaStream_t s) {
   uint32_t* st = status_word();
   if (!st) return FA_ERR_CUDA;
-  const int grid = num_sms();
+  const int grid = paged::decode_grid();
   const long long cap = (long long)c.max_pages * c.page_size;
   const paged::DecodeLayout w = paged::layout(c.B, a.Hq, c.d, cap, a.W != nullptr, grid);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
