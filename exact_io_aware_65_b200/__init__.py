@@ -104,11 +104,15 @@ class FAError(RuntimeError):
 
 
 _lib = None
+# The packed and paged calls of _binding.so (csrc/binding.cpp): the same checks
+# and the same library, without ctypes.  What it does not take (it answers None)
+# goes through the Python code of the call.
+_fast = None
 
 
 def lib() -> ctypes.CDLL:
     """Load libfa.so (build it first with ``python -m exact_io_aware_65_b200.build``)."""
-    global _lib
+    global _lib, _fast
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise FAError(3, f"CUDA library missing at {LIB_PATH}; build it with "
@@ -119,12 +123,24 @@ def lib() -> ctypes.CDLL:
             f.restype = res
             f.argtypes = args
         _lib = L
+        if os.path.exists(os.path.join(_HERE, "_binding.so")):
+            from . import _binding
+
+            _binding.use(L._handle)
+            _fast = _binding
     return _lib
 
 
 def _check(code: int, what: str):
     if code != 0:
         raise FAError(code, what)
+
+
+def _taken(answer, what: str) -> bool:
+    """Whether ``_fast`` made the call; its status, if the library refused."""
+    if answer.__class__ is int:
+        raise FAError(answer, what)
+    return answer is not None
 
 
 def _stream(stream) -> int:
@@ -445,6 +461,11 @@ def fwd_packed(Q, K, V, cu_q, cu_k, mask="none", scale=None, O=None, LSE=None, w
     [B + 1]); mask "none" or "causal" (aligned at each sequence's last query and
     key).  Returns O [Tq, Hq, d] bf16 and LSE [Hq, Tq] fp32; rows that belong to
     no sequence are not written."""
+    kind = _packed_mask(mask)
+    if _fast is not None and stream is None:
+        made = _fast.fwd_packed(Q, K, V, cu_q, cu_k, O, LSE, workspace, kind, scale)
+        if _taken(made, "fa_fwd_packed"):
+            return made
     q = _rows(Q, "Q")
     dev = Q.device
     Tq, Hq, d = Q.shape
@@ -463,7 +484,7 @@ def fwd_packed(Q, K, V, cu_q, cu_k, mask="none", scale=None, O=None, LSE=None, w
         workspace = _empty(need, torch.uint8, dev, stream)
     wp, wn = (None, 0) if workspace is None else _workspace(workspace, need, dev)
     _run("fa_fwd_packed", dev, stream, q, k, v,
-         _int32(cu_q, "cu_q", B + 1, dev), _int32(cu_k, "cu_k", B + 1, dev), B, Tq, Tk, Hq, Hkv, d, _packed_mask(mask),
+         _int32(cu_q, "cu_q", B + 1, dev), _int32(cu_k, "cu_k", B + 1, dev), B, Tq, Tk, Hq, Hkv, d, kind,
          scale, o, LSE.data_ptr(), wp, wn)
     return O, LSE
 
@@ -477,6 +498,11 @@ def bwd_packed(Q, K, V, O, dO, LSE, cu_q, cu_k, mask="none", scale=None, dQ=None
     """The gradients of ``fwd_packed``: dQ [Tq, Hq, d], dK, dV [Tk, Hkv, d]
     (summed over each key head's query heads) from O and LSE of the forward
     with the same mask and scale."""
+    kind = _packed_mask(mask)
+    if _fast is not None and stream is None:
+        made = _fast.bwd_packed(Q, K, V, cu_q, cu_k, O, dO, LSE, dQ, dK, dV, workspace, kind, scale, 1 if deterministic else 0)
+        if _taken(made, "fa_bwd_packed"):
+            return made
     q = _rows(Q, "Q")
     dev = Q.device
     Tq, Hq, d = Q.shape
@@ -500,7 +526,7 @@ def bwd_packed(Q, K, V, O, dO, LSE, cu_q, cu_k, mask="none", scale=None, dQ=None
     wp, wn = _workspace(workspace, need, dev)
     _run("fa_bwd_packed", dev, stream, q, k, v, o, g,
          LSE.data_ptr(), _int32(cu_q, "cu_q", B + 1, dev), _int32(cu_k, "cu_k", B + 1, dev), B, Tq, Tk, Hq, Hkv, d,
-         _packed_mask(mask), scale, 1 if deterministic else 0, dq, dk, dv, wp, wn)
+         kind, scale, 1 if deterministic else 0, dq, dk, dv, wp, wn)
     return dQ, dK, dV
 
 
@@ -548,6 +574,9 @@ def paged_append(K, V, cu_seqlens, lens, k_cache, v_cache, page_table, k_scale=N
     the positions already held and is not changed.  Pools are
     [pages, Hkv, page_size, d], bf16 or float8_e4m3fn (then with fp32 scales
     [Hkv]); page_table is int32 [B, pages]."""
+    if _fast is not None and stream is None:
+        if _taken(_fast.paged_append(K, V, cu_seqlens, lens, k_cache, v_cache, page_table, k_scale, v_scale), "fa_paged_append"):
+            return
     c = _paged_cache(k_cache, v_cache, page_table, k_scale, v_scale)
     dev = k_cache.device
     k = _rows(K, "K", c.Hkv, c.d, device=dev)
@@ -570,6 +599,11 @@ def paged_decode(Q, k_cache, v_cache, page_table, lens, scale=None, k_scale=None
     [B, Hkv, at least pages * page_size]) receives the attention that each key
     drew, summed over its group of query heads, or is raised by it with
     ``accumulate``."""
+    if _fast is not None and stream is None:
+        made = _fast.paged_decode(Q, k_cache, v_cache, page_table, lens, k_scale, v_scale, weights, O, LSE, workspace, scale,
+                                  1 if accumulate else 0)
+        if _taken(made, "fa_paged_decode"):
+            return made
     c = _paged_cache(k_cache, v_cache, page_table, k_scale, v_scale)
     dev, B, d = k_cache.device, c.B, c.d
     q = _rows(Q, "Q", None, d, B, dev)
@@ -600,6 +634,10 @@ def paged_evict(weights, k_cache, v_cache, page_table, lens, table_out, budget, 
     of the call reads).  Returns kept [B, Hkv, budget] int32 (the positions
     kept, then -1) and lens_out [B] int32; ``weights_out`` (fp32
     [B, Hkv, width]) gets the kept rows' weights, then zeros."""
+    if _fast is not None and stream is None:
+        made = _fast.paged_evict(weights, k_cache, v_cache, page_table, lens, table_out, weights_out, kept, lens_out, budget, recent)
+        if _taken(made, "fa_paged_evict"):
+            return made
     c = _paged_cache(k_cache, v_cache, page_table, scales=False)  # 8-bit rows move as they are
     dev, B, Hkv = k_cache.device, c.B, c.Hkv
     cap = c.max_pages * c.page_size
