@@ -12,6 +12,8 @@
 #include <cuda_fp8.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "fa_internal.h"
 #include "sm100.cuh"
 #include "paged.cuh"
@@ -195,8 +197,57 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParams p) {
-  extern __shared__ uint32_t keys[];
+// Moves kept rows [r0, r0 + step) of head h of sequence b, then their weights:
+// a group of ROWB / 16 lanes per row and pool, MOVE_ROWS rows of K and of V in
+// flight per lane.  Row r goes to position r of the table of destination pages.
+constexpr int MOVE_ROWS = 4;
+
+template <int ROWB>
+__device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, int left, int r0, int step) {
+  constexpr int LPR = ROWB / 16;
+  const int groups = blockDim.x / LPR;
+  const int sub = threadIdx.x / LPR, piece = threadIdx.x % LPR;
+  const int* kept = p.kept + ((long long)b * p.Hkv + h) * p.budget;
+  const int end = min(left, r0 + step);
+  for (int r1 = r0; r1 < end; r1 += groups * MOVE_ROWS) {
+    uint4 k[MOVE_ROWS], v[MOVE_ROWS];
+    long long dst[MOVE_ROWS];
+#pragma unroll
+    for (int i = 0; i < MOVE_ROWS; ++i) {
+      const int r = r1 + i * groups + sub;
+      dst[i] = -1;
+      if (r < end) {
+        // (pos < max_pages * page_size; rows past the destination table were refused)
+        const int pos = kept[r], from = p.page(pos), to = p.page(r);
+        const int page = to < p.max_out ? __ldg(p.table_out + b * p.table_out_stride + to) : -1;
+        const long long src =
+            row_offset(p.c, __ldg(p.c.table + b * p.c.table_stride + from), pos - from * p.c.page_size);
+        dst[i] = row_offset(p.c, page, r - to * p.c.page_size);
+        if (src < 0 || dst[i] < 0) {
+          bad_page(p.status);
+          dst[i] = -1;
+        } else {
+          const long long at = h * p.c.head_stride + piece * 16;
+          k[i] = *reinterpret_cast<const uint4*>(p.c.K + src + at);
+          v[i] = *reinterpret_cast<const uint4*>(p.c.V + src + at);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MOVE_ROWS; ++i) {
+      if (dst[i] < 0) continue;
+      const long long at = dst[i] + h * p.c.head_stride + piece * 16;
+      *reinterpret_cast<uint4*>(p.c.K + at) = k[i];
+      *reinterpret_cast<uint4*>(p.c.V + at) = v[i];
+    }
+  }
+  const float* w = p.W + b * p.w_batch + h * p.w_head;
+  float* wo = p.Wout + b * p.wo_batch + h * p.wo_head;
+  for (int r = r0 + threadIdx.x; r < end; r += blockDim.x) wo[r] = __ldg(w + kept[r]);
+}
+
+// The positions that stay; the CTA's (sequence, head) in p.kept, and how many.
+__device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys) {
   __shared__ uint32_t hist[SEL_BINS];
   __shared__ int above_w[32], tie_w[32];
   __shared__ uint32_t sh_digit;
@@ -210,11 +261,11 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParam
   for (int i = left + tid; i < p.budget; i += SEL_THREADS) kept[i] = -1;
   if (n <= p.budget) {
     for (int i = tid; i < n; i += SEL_THREADS) kept[i] = i;
-    return;
+    return left;
   }
   const int old = n - p.recent, pick = p.budget - p.recent;  // old > pick >= 0
   for (int i = tid; i < p.recent; i += SEL_THREADS) kept[pick + i] = old + i;
-  if (pick == 0) return;
+  if (pick == 0) return left;
   const float* w = p.W + b * p.w_batch + h * p.w_head;
   const bool cached = old <= SEL_SMEM_KEYS;
   auto key_at = [&](int i) { return cached ? keys[i] : order_key(__ldg(w + i)); };
@@ -319,57 +370,34 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParam
     at += __popc(keep);
     tie_at += __popc(tie);
   }
+  return left;
 }
 
-// Moves the kept rows: a group of ROWB / 16 lanes per row and pool, four rows
-// of K and of V in flight per lane.  Row r goes to position r of the table of
-// destination pages.
-constexpr int MOVE_THREADS = 256;
-constexpr int MOVE_ROWS = 4;
+// ROWB > 0: the CTA moves its rows too.
+template <int ROWB>
+__global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParams p) {
+  extern __shared__ uint32_t keys[];
+  const int left = select_rows(p, keys);
+  if constexpr (ROWB > 0) {
+    __syncthreads();  // kept
+    const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
+    move_rows<ROWB>(p, b, h, left, 0, left);
+    float* wo = p.Wout + b * p.wo_batch + h * p.wo_head;
+    for (int r = left + threadIdx.x; r < p.wo_len; r += SEL_THREADS) wo[r] = 0.0f;
+  }
+}
 
+// The moves alone: p.chunks blocks a (sequence, head).
+constexpr int MOVE_THREADS = 256;
 template <int ROWB>
 __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const EvictParams p) {
-  constexpr int LPR = ROWB / 16, GROUPS = MOVE_THREADS / LPR, PER = GROUPS * MOVE_ROWS;
+  constexpr int PER = MOVE_THREADS / (ROWB / 16) * MOVE_ROWS;
   const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const int b = bh / p.Hkv, h = bh % p.Hkv;
   const int left = min(clamp_len(p.c, __ldg(p.lens + b)), p.budget);
-  const int sub = threadIdx.x / LPR, piece = threadIdx.x % LPR;
-  const int* kept = p.kept + (long long)bh * p.budget;
-  const int r0 = chunk * PER;
-  uint4 k[MOVE_ROWS], v[MOVE_ROWS];
-  long long dst[MOVE_ROWS];
-#pragma unroll
-  for (int i = 0; i < MOVE_ROWS; ++i) {
-    const int r = r0 + i * GROUPS + sub;
-    dst[i] = -1;
-    if (r < left) {
-      // (pos < max_pages * page_size; rows past the destination table were refused)
-      const int pos = __ldg(kept + r), from = p.page(pos), to = p.page(r);
-      const int page = to < p.max_out ? __ldg(p.table_out + b * p.table_out_stride + to) : -1;
-      const long long src =
-          row_offset(p.c, __ldg(p.c.table + b * p.c.table_stride + from), pos - from * p.c.page_size);
-      dst[i] = row_offset(p.c, page, r - to * p.c.page_size);
-      if (src < 0 || dst[i] < 0) {
-        bad_page(p.status);
-        dst[i] = -1;
-      } else {
-        const long long at = h * p.c.head_stride + piece * 16;
-        k[i] = *reinterpret_cast<const uint4*>(p.c.K + src + at);
-        v[i] = *reinterpret_cast<const uint4*>(p.c.V + src + at);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < MOVE_ROWS; ++i) {
-    if (dst[i] < 0) continue;
-    const long long at = dst[i] + h * p.c.head_stride + piece * 16;
-    *reinterpret_cast<uint4*>(p.c.K + at) = k[i];
-    *reinterpret_cast<uint4*>(p.c.V + at) = v[i];
-  }
-  // the weights of these rows; the rest of the row, shared by the blocks, is zero
-  const float* w = p.W + b * p.w_batch + h * p.w_head;
+  move_rows<ROWB>(p, b, h, left, chunk * PER, PER);
+  // the rest of the weights' row, shared by the blocks, is zero
   float* wo = p.Wout + b * p.wo_batch + h * p.wo_head;
-  for (int r = r0 + threadIdx.x; r < min(left, r0 + PER); r += MOVE_THREADS) wo[r] = __ldg(w + __ldg(kept + r));
   for (long long r = left + (long long)chunk * MOVE_THREADS + threadIdx.x; r < p.wo_len;
        r += (long long)p.chunks * MOVE_THREADS)
     wo[r] = 0.0f;
@@ -431,20 +459,28 @@ fa_status launch_paged_evict(const PagedCache& c, const Evict& e, cudaStream_t s
   // shared memory for the keys a head can have to choose from, when they fit
   const long long most = (long long)c.max_pages * c.page_size - e.recent;
   const int smem = 4 * (int)(most < 0 ? 0 : most < paged::SEL_SMEM_KEYS ? most : paged::SEL_SMEM_KEYS);
-  static std::atomic<uint64_t> done{0};
-  if (!allow_smem(done, (const void*)paged::select_kernel, 4 * paged::SEL_SMEM_KEYS) ||
-      !launch(paged::select_kernel, (unsigned)(c.B * c.Hkv), paged::SEL_THREADS, smem, s, p))
-    return FA_ERR_CUDA;
-  bool ok;
-  auto move = [&](auto kern, int rowb) {
-    const int per = paged::MOVE_THREADS / (rowb / 16) * paged::MOVE_ROWS;
-    p.chunks = (e.budget + per - 1) / per;
-    ok = launch(kern, (unsigned)(c.B * c.Hkv * p.chunks), paged::MOVE_THREADS, 0, s, p);
-  };
+  // A CTA moves the rows it has selected where that is little (sequences
+  // of 500 and 1000 rows cut to 250: 10.3 against 13.3 us), or where there
+  // is a CTA for every SM; else a second kernel moves them with all SMs (eight
+  // caches of 7000-8192 rows cut to 2048: 64 CTAs alone would move 2 MB each).
   const int rowb = c.d * c.elem;
-  if (rowb == 64) move(paged::move_kernel<64>, 64);
-  else if (rowb == 128) move(paged::move_kernel<128>, 128);
-  else move(paged::move_kernel<256>, 256);
+  const long long rows = most + e.recent < e.budget ? most + e.recent : e.budget;
+  const bool fused = c.B * c.Hkv >= num_sms() || 4 * rows * rowb <= 256 * 1024;
+  auto run = [&](auto width) -> bool {
+    constexpr int W = decltype(width)::value;
+    static std::atomic<uint64_t> done[2];
+    auto kern = fused ? paged::select_kernel<W> : paged::select_kernel<0>;
+    if (!allow_smem(done[fused], (const void*)kern, 4 * paged::SEL_SMEM_KEYS) ||
+        !launch(kern, (unsigned)(c.B * c.Hkv), paged::SEL_THREADS, smem, s, p))
+      return false;
+    if (fused) return true;
+    constexpr int PER = paged::MOVE_THREADS / (W / 16) * paged::MOVE_ROWS;
+    p.chunks = (e.budget + PER - 1) / PER;
+    return launch(paged::move_kernel<W>, (unsigned)(c.B * c.Hkv * p.chunks), paged::MOVE_THREADS, 0, s, p);
+  };
+  const bool ok = rowb == 64    ? run(std::integral_constant<int, 64>())
+                  : rowb == 128 ? run(std::integral_constant<int, 128>())
+                                : run(std::integral_constant<int, 256>());
   return ok ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -153,6 +153,20 @@ __host__ __device__ __forceinline__ void next_unit(const Work& k, Walk& w) {
   } while (w.nblk == 0 && w.b + 1 < k.B);
 }
 
+// Whole units only: a CTA takes the units that begin in its share.  w: its walk;
+// next_b: the sequence that holds the first block of the next CTA's share.
+__host__ __device__ __forceinline__ long long unit_boundary(const Walk& w) { return w.blk > 0 ? w.at + (w.nblk - w.blk) : w.at; }
+__host__ __device__ __forceinline__ Walk whole_units(const Work& k, const int* prefix, Walk w, int next_b, long long total,
+                                                     int grid, int cta) {
+  if (w.at >= w.end) return w;
+  if (cta + 1 < grid) w.end = unit_boundary(start_walk(k, prefix, next_b, total, grid, cta + 1));
+  if (w.blk > 0) {
+    w.at = unit_boundary(w);
+    next_unit(k, w);
+  }
+  return w;
+}
+
 }  // namespace paged
 
 inline paged::Cache cache_view(const PagedCache& c) {
