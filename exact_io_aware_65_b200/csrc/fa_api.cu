@@ -365,11 +365,15 @@ fa_status fa_fwd_packed(const fa_rows* Q, const fa_rows* K, const fa_rows* V, co
     return FA_ERR_INVALID_ARG;
   if (Tq == 0) return FA_OK;
   if (!LSE || !aligned(LSE, 4)) return FA_ERR_INVALID_ARG;
-  return launch_fwd_packed(p, q, k, v, o, LSE, (cudaStream_t)stream);
+  const size_t need = fwd_packed_workspace_bytes(B, Tq, Hq, d);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return FA_ERR_WORKSPACE;
+  return launch_fwd_packed(p, q, k, v, o, LSE, workspace, (cudaStream_t)stream);
 }
 
 size_t fa_fwd_packed_workspace_size(int B, int Tq, int Hq, int Hkv, int d) {
-  return 0;
+  if (B <= 0 || Tq <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  if (!packed_sizes_supported(B, Tq, 0, Hq, Hkv)) return 0;
+  return fwd_packed_workspace_bytes(B, Tq, Hq, d);
 }
 
 size_t fa_bwd_packed_workspace_size(int B, int Tq, int Tk, int Hq, int Hkv, int d) {

@@ -112,7 +112,8 @@ struct Cfg {
 // MODE: FIXED, every sequence has N, Nk (and the sizes stay compile-time-free
 // of extra registers); PADDED, per-sequence lengths are read; PACKED, packed
 // rows and grouped heads (the maps of Q, K and V then have a fourth dimension,
-// the head, behind the sequence's first row).
+// the head, behind the sequence's first row); SPLIT, these with the keys of an
+// item divided into parts, which join_kernel joins.
 template <int D, int MODE, int PIPES>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __shared__ __align__(8) uint64_t item_full[2][RING], item_empty[2][RING];
   __shared__ int item_ring[2][RING];
   // PACKED: the producer also passes on what it found the item to be
-  __shared__ int4 item_desc[2][MODE == PACKED ? RING : 1][2];
+  __shared__ int4 item_desc[2][MODE >= PACKED ? RING : 1][2];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
 
@@ -185,13 +186,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // its epilogue, so that it need not stay in registers (76 bytes of spills
   // instead of 148, 497 us instead of 518 for 2 x 8192 tokens of 16 heads; at
   // d = 64 there were more of them that way).
-  constexpr bool REREAD = MODE == PACKED && D == 128;
+  constexpr bool REREAD = MODE >= PACKED && D == 128;
   // The k-th item of pipeline q; idx >= n_items: no more.
   auto read_item = [&](int q, uint32_t slot, int& idx, Item& it) {
     idx = *reinterpret_cast<volatile int*>(&item_ring[q][slot]);
-    if (MODE == PACKED) {
+    if (MODE >= PACKED) {
       const int4 a = item_desc[q][slot][0], b = item_desc[q][slot][1];
-      it.q0 = a.x;
+      it.q0 = MODE == SPLIT ? a.x & 0xffffff : a.x;
       it.q1 = a.y & 0x7fffffff;
       it.has1 = a.y < 0;
       it.h0 = a.z;
@@ -202,6 +203,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       it.Lk = b.w;
       it.nkb = pack::tiles(it.Lk);
       it.off = it.nkb - pack::tiles(it.Lq);
+      if (MODE == SPLIT) {
+        it.part = a.x >> 24;
+        take_part(p, it);
+      }
     }
   };
   auto take_item = [&](int q, uint32_t k, int& idx, Item& it) -> bool {
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (!mbar_wait(&item_full[q][slot], (k / RING) & 1, w)) return false;
     read_item(q, slot, idx, it);
     mbar_arrive(&item_empty[q][slot]);
-    if (MODE != PACKED && idx < p.n_items) it = item_at<MODE>(p, idx);
+    if (MODE < PACKED && idx < p.n_items) it = item_at<MODE>(p, idx);
     return true;
   };
   auto give_back = [&](int q, uint32_t k) {
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (!mbar_wait_warp(&item_full[q][slot], (k / RING) & 1, w)) return false;
     read_item(q, slot, idx, it);
     if (!REREAD) give_back(q, k);
-    if (MODE != PACKED && idx < p.n_items) it = item_at<MODE>(p, idx);
+    if (MODE < PACKED && idx < p.n_items) it = item_at<MODE>(p, idx);
     return true;
   };
 
@@ -235,17 +240,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ------------------------------------------------------------ producer
     // (of pipeline q).  One thread; PACKED: the warp looks the items up
     // together, and lane 0 issues the copies.
-    if (MODE == PACKED || lane == 0) {
+    if (MODE >= PACKED || lane == 0) {
       const int q = warp == 0 ? 0 : 1;
-      const bool lead = MODE != PACKED || lane == 0;
+      const bool lead = MODE < PACKED || lane == 0;
       auto await = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return MODE == PACKED ? mbar_wait_warp(bar, parity, w) : mbar_wait(bar, parity, w);
+        return MODE >= PACKED ? mbar_wait_warp(bar, parity, w) : mbar_wait(bar, parity, w);
       };
       // rows [y, y + 128) of a head's sequence (of head bh), 64 columns a copy
       auto load = [&](uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int y, int start, int head) {
 #pragma unroll
         for (int c = 0; c < C::CHUNKS; ++c) {
-          if (MODE == PACKED) tma_load_4d(dst + c * C::CHUNK_BYTES, m, bar, c * 64, y, start, head);
+          if (MODE >= PACKED) tma_load_4d(dst + c * C::CHUNK_BYTES, m, bar, c * 64, y, start, head);
           else tma_load_3d(dst + c * C::CHUNK_BYTES, m, bar, c * 64, y, head);
         }
       };
@@ -260,28 +265,36 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // Pipeline q of CTA b starts on item NPIPE b + q, then claims items
         // NPIPE gridDim.x, NPIPE gridDim.x + 1, ...
         int idx = (int)(blockIdx.x * C::NPIPE) + q;
-        if (item_iter > 0) {
-          if (lead) idx = (int)(gridDim.x * C::NPIPE) + (int)atomicAdd(&g_claim[p.slot], 1u);
-          if (MODE == PACKED) idx = __shfl_sync(0xffffffffu, idx, 0);
-        }
-        if (idx > p.n_items) idx = p.n_items;
         Item it;
-        if (MODE == PACKED) {
-          int b;
-          pack::Seq sq;
-          pack::Place at;
-          if (idx < p.n_items && pack::locate(p.pk, walk, idx, p.n_items, [&](const pack::Seq& x) { return packed_units(p, x); },
-                                              [](const pack::Seq& x) { return x.Lk; }, b, sq, at))
-            it = packed_item(p, sq, at);
-          else
-            idx = p.n_items;
-        } else if (idx < p.n_items) {
-          it = item_at<MODE>(p, idx);
+        for (bool more = item_iter > 0;; more = true) {
+          if (more) {
+            if (lead) idx = (int)(gridDim.x * C::NPIPE) + (int)atomicAdd(&g_claim[p.slot], 1u);
+            if (MODE >= PACKED) idx = __shfl_sync(0xffffffffu, idx, 0);
+          }
+          if (idx > p.n_items) idx = p.n_items;
+          if (MODE >= PACKED) {
+            int b;
+            pack::Seq sq;
+            pack::Place at;
+            if (idx < p.n_items && pack::locate(p.pk, walk, idx, p.n_items, [&](const pack::Seq& x) { return packed_units(p, x); },
+                                                [](const pack::Seq& x) { return x.Lk; }, b, sq, at)) {
+              it = packed_item(p, sq, at);
+              if (MODE == SPLIT) {
+                take_part(p, it);
+                if (it.part >= it.parts) continue;  // the item has fewer parts: nothing to do
+              }
+            } else {
+              idx = p.n_items;
+            }
+          } else if (idx < p.n_items) {
+            it = item_at<MODE>(p, idx);
+          }
+          break;
         }
         if (lead) {
           item_ring[q][slot] = idx;
-          if (MODE == PACKED && idx < p.n_items) {
-            item_desc[q][slot][0] = make_int4(it.q0, it.q1 | (it.has1 ? (int)0x80000000 : 0), it.h0, it.h1);
+          if (MODE >= PACKED && idx < p.n_items) {
+            item_desc[q][slot][0] = make_int4(MODE == SPLIT ? it.q0 | it.part << 24 : it.q0, it.q1 | (it.has1 ? (int)0x80000000 : 0), it.h0, it.h1);
             item_desc[q][slot][1] = make_int4(it.sq, it.Lq, it.sk, it.Lk);
           }
           mbar_arrive(&item_full[q][slot]);
@@ -290,17 +303,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         q_loading = false;
         ok = await(&q_empty[q], (item_iter & 1) ^ 1);
         if (!ok) break;
-        const int yq = MODE == PACKED ? -pack::pad(it.Lq) : 0, yk = MODE == PACKED ? -pack::pad(it.Lk) : 0;
-        const int hk = MODE == PACKED ? it.h0 / p.pk.G : it.bh;
+        const int yq = MODE >= PACKED ? -pack::pad(it.Lq) : 0, yk = MODE >= PACKED ? -pack::pad(it.Lk) : 0;
+        const int hk = MODE >= PACKED ? it.h0 / p.pk.G : it.bh;
         if (lead) {
           mbar_arrive_expect_tx(&q_full[q], C::TILE_BYTES * (it.has1 ? 2 : 1));
-          load(sQ + q * C::TILE_BYTES, &mapQ, &q_full[q], yq + it.q0 * BM, it.sq, MODE == PACKED ? it.h0 : it.bh);
+          load(sQ + q * C::TILE_BYTES, &mapQ, &q_full[q], yq + it.q0 * BM, it.sq, MODE >= PACKED ? it.h0 : it.bh);
           if (it.has1)
-            load(sQ + C::TILE_BYTES, &mapQ, &q_full[q], yq + it.q1 * BM, it.sq, MODE == PACKED ? it.h1 : it.bh);
+            load(sQ + C::TILE_BYTES, &mapQ, &q_full[q], yq + it.q1 * BM, it.sq, MODE >= PACKED ? it.h1 : it.bh);
         }
         q_loading = true;
         const int e = kv_end<MODE>(p, it);
-        for (int j = next_union<MODE>(p, it, 0); ok && j < e; j = next_union<MODE>(p, it, j + 1)) {
+        for (int j = next_union<MODE>(p, it, kv_begin<MODE>(it)); ok && j < e; j = next_union<MODE>(p, it, j + 1)) {
           for (int kv = 0; kv < 2; ++kv) {
             const uint32_t slot = kv_iter % C::NSLOT;
             ok = await(&kv_empty[q][slot], ((kv_iter / C::NSLOT) & 1) ^ 1);
@@ -402,7 +415,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
           tc_fence_after();
           const int e = kv_end<MODE>(p, it);
-          int j = next_union<MODE>(p, it, 0), jp = -1;
+          int j = next_union<MODE>(p, it, kv_begin<MODE>(it)), jp = -1;
           if (j >= e) tc_commit(&q_empty[q]);  // no key tile: Q was not read
           bool first_pv = true;
           while (ok && (j < e || jp >= 0)) {
@@ -457,7 +470,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         const int e = kv_end<MODE>(p, it);
-        int j = next_union<MODE>(p, it, 0);
+        int j = next_union<MODE>(p, it, kv_begin<MODE>(it));
         int jn = j < e ? next_union<MODE>(p, it, j + 1) : e;  // the key tile after j
         bool first_pv[2] = {true, true};
         // Q is read only by the QK^T products: it goes back to the producer
@@ -583,7 +596,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         return e;
       };
-      for (int j = next_key(0); j < e; j = next_key(j + 1)) {
+      for (int j = next_key(kv_begin<MODE>(it)); j < e; j = next_key(j + 1)) {
         ok = mbar_wait_warp(&s_full[t], s_cnt & 1, w);
         if (!ok) break;
         ++s_cnt;
@@ -603,7 +616,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // keys <= row + off
         const int key0 = j * BN;
         int lim;
-        if (MODE == PACKED) {
+        if (MODE >= PACKED) {
           // tiles counted from the end: the causal boundary is a tile's
           // diagonal, and the columns before the first key are in tile 0
           lim = p.mask_kind == FA_MASK_CAUSAL && j == qt + it.off ? r + 1 : BN;
@@ -724,26 +737,49 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_after();
       // false for a row that sees no key, or padding
       // (PACKED: a NaN that a row saw is kept)
-      const bool live = MODE == PACKED ? l != 0.0f : l > 0.0f && row < it.Lq;
+      const bool live = MODE >= PACKED ? l != 0.0f : l > 0.0f && row < it.Lq;
       if (REREAD) {
         read_item(0, k % RING, idx, it);
         give_back(0, k);
       }
       // PACKED: the row's place in the packed tensors (negative: before the
       // sequence), and its head
-      const int prow = MODE == PACKED ? row - pack::pad(it.Lq) : 0;
-      const int head = MODE == PACKED ? ((C::DUAL || t == 0) ? it.h0 : it.h1) : it.bh;
+      const int prow = MODE >= PACKED ? row - pack::pad(it.Lq) : 0;
+      const int head = MODE >= PACKED ? ((C::DUAL || t == 0) ? it.h0 : it.h1) : it.bh;
       const float inv_l = live ? 1.0f / l : 0.0f;
-      {
+      bool partial = false;
+      if constexpr (MODE == SPLIT) {
+        partial = it.parts > 1;
+        if (partial && prow >= 0 && FA_IN_BOUNDS(p.status, it.sq + prow, 1, p.pk.Tq)) {
+          p.part_ml[((size_t)it.part * p.pk.Hq + head) * p.pk.Tq + it.sq + prow] = make_float2(m, l);
+        }
+        if (partial) {
+          float4* row_o = reinterpret_cast<float4*>(p.part_o + (((long long)it.part * p.pk.Hq + head) * p.pk.Tq + it.sq + prow) * D);
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t v[32];
+            FA_TMEM_LD_X32(t_o + c, v);
+            tc_wait_ld();
+            if (prow >= 0 && FA_IN_BOUNDS(p.status, it.sq + prow, 1, p.pk.Tq)) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                row_o[c / 4 + i] = live ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                      __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
+        }
+      }
+      if (!partial) {
         // Per 64 columns: lane i puts row i of the warp's 32 (128 bytes:
         // eight 16-byte chunks, chunk k at slot k ^ (i & 7), which is the
         // 128-byte swizzle), then lane 0 stores the 32 x 64 box with one
         // tensor store (rows past N are not written).
         uint8_t* ws = sO + (warp - 4) * 4096;
-        const int row0 = MODE == PACKED ? it.sq + prow - lane : qt * BM + quarter * 32;
+        const int row0 = MODE >= PACKED ? it.sq + prow - lane : qt * BM + quarter * 32;
         // PACKED: a box that begins before the sequence leaves row by row (a
         // tensor store would write the rows of the sequence before)
-        const bool by_row = MODE == PACKED && prow - lane < 0;
+        const bool by_row = MODE >= PACKED && prow - lane < 0;
 #pragma unroll
         for (int g = 0; g < D / 64; ++g) {
           if (lane == 0) bulk_wait_read_all();  // the warp's previous store has read the buffer
@@ -784,7 +820,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
       }
-      if (MODE == PACKED) {
+      if (partial) {
+        // the join writes O and LSE
+      } else if (MODE >= PACKED) {
         const size_t at = (size_t)head * p.pk.Tq + it.sq + prow;
         if (prow >= 0 && FA_IN_BOUNDS(p.status, at, 1, (size_t)p.pk.Hq * p.pk.Tq))
           p.LSE[at] = live ? (m + log2f(l)) * LN2 : -INFINITY;
@@ -801,6 +839,64 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of a query tile's rows, in order: JOIN_ROWS rows a block (a
+// warp a row at a time), JOIN_BLOCKS blocks a (slot, head).  Rows whose item had
+// one part have been written already.
+constexpr int MAX_PARTS = 32;  // a lane holds a part's maximum and sum
+constexpr int JOIN_ROWS = 16, JOIN_BLOCKS = BM / JOIN_ROWS;
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const Params p) {
+  const int tile = blockIdx.x / JOIN_BLOCKS;
+  const int slot = tile / p.pk.Hq, h = tile % p.pk.Hq;
+  const int b = pack::sequence_of_slot(p.pk, slot);
+  if (b < 0) return;
+  const pack::Seq s = pack::seq_at(p.pk, b);
+  const int i = slot - pack::slot_base(s.sq, b), nq = pack::tiles(s.Lq), nk = pack::tiles(s.Lk);
+  if (i >= nq) return;
+  const int parts = parts_of(p, packed_end(p, nk, nk - nq, last_tile(p, nq, i)));
+  if (parts == 1) return;
+  constexpr int E = D / 32;  // columns a lane
+  const int lane = threadIdx.x & 31, first = (blockIdx.x % JOIN_BLOCKS) * JOIN_ROWS;
+  const size_t rows = (size_t)p.pk.Hq * p.pk.Tq;
+#pragma unroll
+  for (int r = threadIdx.x >> 5; r < JOIN_ROWS; r += 8) {
+    const int n = i * BM + first + r - pack::pad(s.Lq);
+    if (n < 0 || !FA_IN_BOUNDS(p.status, s.sq + n, 1, p.pk.Tq)) continue;
+    const size_t row = (size_t)h * p.pk.Tq + s.sq + n;
+    const float2 ml = lane < parts ? p.part_ml[lane * rows + row] : make_float2(-INFINITY, 0.0f);
+    float M = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float factor = ex2_approx(ml.x - (M == -INFINITY ? 0.0f : M));
+    float L = ml.y * factor;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    float acc[E] = {};
+#pragma unroll 8
+    for (int u = 0; u < parts; ++u) {
+      const float f = __shfl_sync(0xffffffffu, factor, u);
+      const float* o = p.part_o + (u * rows + row) * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(o);
+        acc[0] = fmaf(x.x, f, acc[0]);
+        acc[1] = fmaf(x.y, f, acc[1]);
+        acc[2] = fmaf(x.z, f, acc[2]);
+        acc[3] = fmaf(x.w, f, acc[3]);
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(o);
+        acc[0] = fmaf(x.x, f, acc[0]);
+        acc[1] = fmaf(x.y, f, acc[1]);
+      }
+    }
+    const bool live = L != 0.0f;  // (a NaN that the row saw is kept)
+    const float inv = live ? 1.0f / L : 0.0f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + (long long)(s.sq + n) * p.o_row + h * p.o_head + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = live ? pack_bf16x2(acc[e] * inv, acc[e + 1] * inv) : 0u;
+    if (lane == 0) p.LSE[row] = live ? (M + log2f(L)) * LN2 : -INFINITY;
   }
 }
 
@@ -864,8 +960,36 @@ fa_status launch_fwd(const Problem& pr, const void* Q, const void* K, const void
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// Parts that the key tiles of a work item are divided into, at most: where the
+// query tiles give no more than every other pipeline an item (few heads, or a few
+// new tokens against a long history), as many as give each of them four.
+static int packed_key_parts(int B, int Tq, int Hq, int d) {
+  const bool dual = d == 64;
+  const long long tiles = Tq / 128 + (B + 1) / 2;
+  const long long items = dual ? tiles * Hq : (tiles * Hq + 1) / 2, pipes = (long long)num_sms() * (dual ? 2 : 1);
+  if (2 * items > pipes) return 1;
+  const long long n = (4 * pipes + items - 1) / items;
+  return (int)(n < fwd::MAX_PARTS ? n : fwd::MAX_PARTS);
+}
+
+struct SplitLayout {
+  int parts;
+  size_t ml, total;
+};
+static SplitLayout split_layout(int B, int Tq, int Hq, int d) {
+  SplitLayout l{packed_key_parts(B, Tq, Hq, d), 0, 0};
+  if (l.parts > 1) {
+    const size_t rows = (size_t)l.parts * Hq * Tq;
+    l.ml = (rows * d * sizeof(float) + 255) & ~size_t(255);
+    l.total = l.ml + ((rows * sizeof(float2) + 255) & ~size_t(255));
+  }
+  return l;
+}
+
+size_t fwd_packed_workspace_bytes(int B, int Tq, int Hq, int d) { return split_layout(B, Tq, Hq, d).total; }
+
 fa_status launch_fwd_packed(const PackedProblem& pr, const Rows& Q, const Rows& K, const Rows& V, const Rows& O,
-                            float* LSE, cudaStream_t s) {
+                            float* LSE, void* workspace, cudaStream_t s) {
   uint32_t* st = status_word();
   if (!st) return FA_ERR_CUDA;
   const Pack& k = pr.pk;
@@ -882,8 +1006,14 @@ fa_status launch_fwd_packed(const PackedProblem& pr, const Rows& Q, const Rows& 
   const bool dual = pr.d == 64;
   p.tiles_per_item = dual ? 1 : 2;
   p.by_heads = !dual && k.G % 2 == 0;
+  // Divided keys only where an average sequence has two parts' worth of them.
+  const SplitLayout split = split_layout(k.B, k.Tq, k.Hq, pr.d);
+  const bool divide = split.parts > 1 && k.Tk / 128 / k.B >= 16;
+  p.parts = divide ? split.parts : 1;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + split.ml);
   // at most: the sequences' tiles number no more than the slots
-  p.n_items = (int)(pack::slots(k.Tq, k.B) * (p.by_heads ? k.Hq / 2 : k.Hq));
+  p.n_items = (int)(pack::slots(k.Tq, k.B) * (p.by_heads ? k.Hq / 2 : k.Hq) * p.parts);
   p.mask_kind = pr.mask_kind;
   p.scale_log2 = pr.scale_log2;
   p.O = static_cast<__nv_bfloat16*>(O.data);
@@ -896,15 +1026,23 @@ fa_status launch_fwd_packed(const PackedProblem& pr, const Rows& Q, const Rows& 
   const int npipe = dual ? 2 : 1;
   const int want = (p.n_items + npipe - 1) / npipe;
   const int grid = want < num_sms() ? want : num_sms();
-  static std::atomic<uint64_t> done[2];  // d = 64, 128
-  auto run = [&](auto kern, int smem) -> bool {
-    return allow_smem(done[pr.d == 128], (const void*)kern, smem) &&
+  auto run = [&](auto kern, std::atomic<uint64_t>& done, int smem) -> bool {
+    return allow_smem(done, (const void*)kern, smem) &&
            launch(kern, (unsigned)grid, fwd::NUM_THREADS, smem, s, mQ, mK, mV, mO, p);
   };
-  if (!(dual ? run(fwd::fwd_kernel<64, PACKED, 2>, fwd::Cfg<64, 2>::SMEM_BYTES)
-             : run(fwd::fwd_kernel<128, PACKED, 1>, fwd::Cfg<128, 1>::SMEM_BYTES)))
-    return FA_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  static std::atomic<uint64_t> done[4];
+  bool ok;
+  if (dual)
+    ok = divide ? run(fwd::fwd_kernel<64, SPLIT, 2>, done[0], fwd::Cfg<64, 2>::SMEM_BYTES)
+                : run(fwd::fwd_kernel<64, PACKED, 2>, done[1], fwd::Cfg<64, 2>::SMEM_BYTES);
+  else
+    ok = divide ? run(fwd::fwd_kernel<128, SPLIT, 1>, done[2], fwd::Cfg<128, 1>::SMEM_BYTES)
+                : run(fwd::fwd_kernel<128, PACKED, 1>, done[3], fwd::Cfg<128, 1>::SMEM_BYTES);
+  if (ok && divide) {
+    const unsigned blocks = (unsigned)(pack::slots(k.Tq, k.B) * k.Hq * fwd::JOIN_BLOCKS);
+    ok = dual ? launch(fwd::join_kernel<64>, blocks, 256, 0, s, p) : launch(fwd::join_kernel<128>, blocks, 256, 0, s, p);
+  }
+  return ok ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace fa

@@ -79,7 +79,8 @@ int num_sms();
 fa_status launch_fwd(const Problem& p, const void* Q, const void* K, const void* V, void* O, float* LSE,
                      cudaStream_t s);
 fa_status launch_fwd_packed(const PackedProblem& p, const Rows& Q, const Rows& K, const Rows& V, const Rows& O,
-                            float* LSE, cudaStream_t s);
+                            float* LSE, void* workspace, cudaStream_t s);
+size_t fwd_packed_workspace_bytes(int B, int Tq, int Hq, int d);
 // stage < 0: all three stages; otherwise only the given one (0, 1 or 2).
 fa_status launch_bwd(const Problem& p, const void* Q, const void* K, const void* V, const void* O,
                      const void* dO, const float* LSE, void* dQ, void* dK, void* dV, void* workspace,

@@ -41,6 +41,11 @@ struct Params {
   int by_heads;   // PACKED: an item's two tiles are two heads' of one query tile
   int d;
   long long o_row, o_head;  // PACKED: strides of O, elements
+  // SPLIT: parts of an item's key tiles, at most; each leaves its unnormalised O
+  // [parts][Hq][Tq][d] and (m, l) [parts][Hq][Tq].
+  int parts;
+  float* part_o;
+  float2* part_ml;
 };
 
 // Heads per scheduling group.  The group's K and V tiles are the forward's
@@ -62,6 +67,7 @@ struct Item {
   // PACKED: the heads of the item's tiles, the sequence's first query row and
   // key; off counts tiles.
   int h0, h1, sq, sk;
+  int part, parts, j0, j1;  // SPLIT: the item's part of its parts, and its key tiles
 };
 
 // Work item idx -> (head, pair of query tiles, or one query tile).  Heads are taken in groups
@@ -96,6 +102,26 @@ __host__ __device__ __forceinline__ Item item_at(const Params& p, int idx) {
   return it;
 }
 
+// One past the last key tile that query tile qt of a packed sequence sees.
+__host__ __device__ __forceinline__ int packed_end(const Params& p, int nkb, int off, int qt) {
+  return p.mask_kind == FA_MASK_CAUSAL ? max(0, min(nkb, qt + off + 1)) : nkb;
+}
+
+// SPLIT: the parts that `tiles` key tiles are divided into: at least eight tiles
+// each, since a part costs about two tiles' time before and after them.
+__host__ __device__ __forceinline__ int parts_of(const Params& p, int tiles) { return max(1, min(p.parts, tiles / 8)); }
+// The later query tile of the item that query tile qt of nq belongs to.
+__host__ __device__ __forceinline__ int last_tile(const Params& p, int nq, int qt) {
+  return p.tiles_per_item == 2 && !p.by_heads ? nq - 1 - (nq - 1 - qt) / 2 * 2 : qt;
+}
+// The part's key tiles (none for a part past the item's parts).
+__host__ __device__ __forceinline__ void take_part(const Params& p, Item& it) {
+  const int e = packed_end(p, it.nkb, it.off, it.has1 ? it.q1 : it.q0);
+  it.parts = parts_of(p, e);
+  it.j0 = it.part < it.parts ? e * it.part / it.parts : 0;
+  it.j1 = it.part < it.parts ? e * (it.part + 1) / it.parts : 0;
+}
+
 // Packed sequences.  An item's one or two query tiles: at d = 64 one; at
 // d = 128 one query tile of two heads that share their keys where the heads of
 // a key head come in pairs (both see the same keys, and a sequence of one tile
@@ -104,16 +130,18 @@ __host__ __device__ __forceinline__ pack::Units packed_units(const Params& p, co
   pack::Units u;
   const int nq = pack::tiles(s.Lq), per = p.by_heads ? 2 : 1;
   u.tiles = p.tiles_per_item == 2 && !p.by_heads ? (nq + 1) / 2 : nq;
-  u.heads = p.pk.Hq / per;
+  u.heads = p.pk.Hq / per * p.parts;
   // the heads of whole key heads, their K and V kept to about 32 MiB (as sched_group)
   const long long fit = (32LL << 20) / (4LL * max(s.Lk, 1) * p.d);
   const long long least = (8 + p.pk.G - 1) / p.pk.G;  // 8 query heads
-  u.group = (int)min((long long)p.pk.Hkv, max(fit, least)) * p.pk.G / per;
+  u.group = (int)min((long long)p.pk.Hkv, max(fit, least)) * p.pk.G / per * p.parts;
   return u;
 }
 
-__host__ __device__ __forceinline__ Item packed_item(const Params& p, const pack::Seq& s, const pack::Place& at) {
+__host__ __device__ __forceinline__ Item packed_item(const Params& p, const pack::Seq& s, const pack::Place& place) {
   Item it;
+  const pack::Place at{place.tile, place.head / p.parts};
+  it.part = place.head % p.parts;
   const int nq = pack::tiles(s.Lq);
   it.bh = 0;
   it.Lq = s.Lq;
@@ -148,7 +176,7 @@ __host__ __device__ __forceinline__ int causal_last_key(const Item& it, int qt) 
 template <int MODE>
 __host__ __device__ __forceinline__ bool member(const Params& p, const Item& it, int qt, int j) {
   if (MODE == PADDED && (qt * BM >= it.Lq || j >= it.nkb)) return false;
-  if (MODE == PACKED) return j < it.nkb && (p.mask_kind != FA_MASK_CAUSAL || j <= qt + it.off);
+  if (MODE >= PACKED) return j < it.nkb && (p.mask_kind != FA_MASK_CAUSAL || j <= qt + it.off);
   if (p.mask_kind == FA_MASK_CAUSAL) return j * BN <= causal_last_key(it, qt);
   if (p.mask_kind == FA_MASK_BLOCK)
     return FA_IN_BOUNDS(p.status, (size_t)qt * p.nk + j, 1, (size_t)p.nq * p.nk) &&
@@ -160,13 +188,19 @@ __host__ __device__ __forceinline__ bool member(const Params& p, const Item& it,
 template <int MODE>
 __host__ __device__ __forceinline__ int kv_end(const Params& p, const Item& it) {
   if (MODE == PADDED && it.q0 * BM >= it.Lq) return 0;
-  if (MODE == PACKED)
-    return p.mask_kind == FA_MASK_CAUSAL ? max(0, min(it.nkb, (it.has1 ? it.q1 : it.q0) + it.off + 1)) : it.nkb;
+  if (MODE == SPLIT) return it.j1;
+  if (MODE >= PACKED) return packed_end(p, it.nkb, it.off, it.has1 ? it.q1 : it.q0);
   if (p.mask_kind == FA_MASK_CAUSAL) {
     const int last = causal_last_key(it, (it.has1 && (MODE != PADDED || it.q1 * BM < it.Lq)) ? it.q1 : it.q0);
     return last < 0 ? 0 : min(it.nkb, last / BN + 1);
   }
   return it.nkb;
+}
+
+// The first key tile of the item's key loop.
+template <int MODE>
+__host__ __device__ __forceinline__ int kv_begin(const Item& it) {
+  return MODE == SPLIT ? it.j0 : 0;
 }
 
 // Next key tile >= j needed by either query tile of the item (kv_end if none).

@@ -21,8 +21,9 @@
 namespace fa {
 
 // Instantiations of the attention kernels: one length for all sequences,
-// padded storage with a length each, packed rows.
-enum : int { FIXED = 0, PADDED = 1, PACKED = 2 };
+// padded storage with a length each, packed rows, and (forward) packed rows whose
+// keys are divided into parts.
+enum : int { FIXED = 0, PADDED = 1, PACKED = 2, SPLIT = 3 };
 
 struct Pack {
   const int* cu_q;  // [B + 1] first rows of the sequences

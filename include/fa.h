@@ -229,6 +229,9 @@ typedef struct {
  *      head are summed over its query heads in fp32 and rounded once.  dK and dV
  *      have the same bits on every run, dQ with deterministic != 0 (as
  *      fa_bwd_qk_deterministic).
+ *      The forward's workspace (0 bytes for most sizes) is for calls with too few
+ *      query tiles to fill the GPU: the keys are then divided among more work
+ *      items, and their parts joined in a fixed order.
  * Tq and Tk up to 2^28, (T / 128 + B + 1) Hq up to 2^29 (FA_ERR_UNSUPPORTED above). */
 size_t fa_fwd_packed_workspace_size(int B, int Tq, int Hq, int Hkv, int d);
 fa_status fa_fwd_packed(const fa_rows* Q, const fa_rows* K, const fa_rows* V, const int* cu_q,

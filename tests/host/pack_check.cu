@@ -45,6 +45,7 @@ void check(const Pack& k, int d, int kind, int parts) {
   f.mask_kind = kind;
   f.tiles_per_item = d == 64 ? 1 : 2;
   f.by_heads = d == 128 && k.G % 2 == 0;
+  f.parts = 1;
   fa::bwd::Params w = {};
   w.pk = k;
   w.d = d;
@@ -93,6 +94,35 @@ void check(const Pack& k, int d, int kind, int parts) {
     }
     for (int x : seen)
       if (x != 1) fail("tile missed", b, x, 0, 0);
+    // ---- forward with divided keys: an item's parts cover its key tiles once,
+    // and the join counts the parts that the items have
+    fa::fwd::Params g = f;
+    g.parts = 1 + rnd(6);
+    std::vector<int> visits((size_t)k.Hq * nq * std::max(nk, 1), 0), parts_seen((size_t)k.Hq * nq, 0);
+    const P::Units ug = fa::fwd::packed_units(g, s);
+    for (int r = 0; r < ug.tiles * ug.heads; ++r) {
+      fa::fwd::Item it = fa::fwd::packed_item(g, s, P::place_of(ug, r));
+      fa::fwd::take_part(g, it);
+      if (it.part >= it.parts) {
+        if (it.j0 < it.j1) fail("part past the parts", b, r, it.part, it.parts);
+        continue;
+      }
+      for (int t = 0; t < (it.has1 ? 2 : 1); ++t) {
+        const int q = t ? it.q1 : it.q0, h = t ? it.h1 : it.h0;
+        parts_seen[(size_t)h * nq + q]++;
+        for (int j = fa::fwd::kv_begin<fa::SPLIT>(it); j < fa::fwd::kv_end<fa::SPLIT>(g, it); ++j) {
+          if (j >= nk) fail("part's key tile", b, r, j, nk);
+          else visits[((size_t)h * nq + q) * nk + j]++;
+        }
+      }
+    }
+    for (int h = 0; h < k.Hq; ++h)
+      for (int q = 0; q < nq; ++q) {
+        const int e = fa::fwd::packed_end(g, nk, nk - nq, fa::fwd::last_tile(g, nq, q));
+        if (parts_seen[(size_t)h * nq + q] != fa::fwd::parts_of(g, e)) fail("parts", b, h, q, parts_seen[(size_t)h * nq + q]);
+        for (int j = 0; j < nk; ++j)
+          if (visits[((size_t)h * nq + q) * nk + j] != (j < e)) fail("divided keys", b, h, q, j);
+      }
     // ---- backward
     std::vector<int> done((size_t)k.Hkv * parts * nk, 0), pairs((size_t)k.Hq * nq * nk, 0);
     const P::Units v = fa::bwd::packed_units(w, s);
@@ -143,6 +173,15 @@ int main() {
   static const int lens[] = {0, 1, 2, 63, 64, 127, 128, 129, 200, 255, 256, 257, 300, 500};
   static const int heads[][2] = {{1, 1}, {4, 4}, {8, 2}, {6, 2}, {5, 1}, {16, 1}, {10, 2}};
   int cases = 0;
+  for (int n = 0; n < 30; ++n) {  // long enough to be divided
+    std::vector<int> cq(1, 0), ck(1, 0);
+    cq.push_back(1 + rnd(3000));
+    ck.push_back(1 + rnd(6000));
+    const int* h = heads[rnd(7)];
+    Pack k{cq.data(), ck.data(), 1, cq.back(), ck.back(), h[0], h[1], h[0] / h[1]};
+    check(k, rnd(2) ? 64 : 128, rnd(2) ? FA_MASK_CAUSAL : FA_MASK_NONE, 1 + rnd(k.G));
+    ++cases;
+  }
   for (int n = 0; n < 400; ++n) {
     const int B = 1 + rnd(5);
     std::vector<int> cq(1, rnd(2) ? rnd(200) : 0), ck(1, rnd(2) ? rnd(200) : 0);

@@ -59,8 +59,12 @@ CASES = [
     ([0, 0], [17, 0], 4, 4),                  # nobody asks
     ([700], [700], 16, 1),
     ([640, 384, 512], [0, 0, 0], 10, 2),      # whole tiles
+    ([1], [4999], 8, 2),                      # few query tiles, many keys: divided between work items
+    ([200, 3, 0], [4000, 2500, 3000], 3, 1),  # (pairs of query tiles at d = 128)
+    ([2300], [0], 4, 1),
+    ([130, 1, 129, 2], [2100, 0, 6000, 1], 6, 2),  # (some sequences divided, some not)
 ]
-IDS = [f"{len(c[0])}seq-max{max(c[0])}-{c[2]}over{c[3]}" for c in CASES]
+IDS = [f"{len(c[0])}seq-max{max(c[0])}+{max(c[1])}-{c[2]}over{c[3]}" for c in CASES]
 
 
 @pytest.mark.parametrize("mask", ["causal", "none"])

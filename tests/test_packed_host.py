@@ -40,11 +40,14 @@ def test_schedules_and_masks_of_packed_sequences(tmp_path):
     ("pack.cuh", "s.Lk = min(max(ld_ro(k.cu_k + b + 1), s.sk), k.Tk) - s.sk;", "s.Lk = ld_ro(k.cu_k + b + 1) - s.sk;"),
     ("pack.cuh", "const int gsize = min(u.group, u.heads - g * u.group);", "const int gsize = u.group;"),
     ("fwd_sched.cuh", "it.q0 = it.has1 ? it.q1 - 1 : 0;", "it.q0 = it.q1 - 1;"),
-    ("fwd_sched.cuh", "(it.has1 ? it.q1 : it.q0) + it.off + 1", "(it.has1 ? it.q1 : it.q0) + it.off"),
+    ("fwd_sched.cuh", "max(0, min(nkb, qt + off + 1)) : nkb;", "max(0, min(nkb, qt + off)) : nkb;"),
+    ("fwd_sched.cuh", "it.j1 = it.part < it.parts ? e * (it.part + 1) / it.parts : 0;",
+     "it.j1 = it.part < it.parts ? e / it.parts * (it.part + 1) : 0;"),
+    ("fwd_sched.cuh", "nq - 1 - (nq - 1 - qt) / 2 * 2 : qt;", "qt / 2 * 2 + 1 : qt;"),
     ("bwd_sched.cuh", "return p.mask_kind == FA_MASK_CAUSAL ? max(0, it.j - it.off) : 0;",
      "return p.mask_kind == FA_MASK_CAUSAL ? max(0, it.j) : 0;"),
     ("bwd_sched.cuh", "it.g1 = (it.part + 1) * p.pk.G / p.parts;", "it.g1 = it.g0 + p.pk.G / p.parts;"),
-], ids=["pad", "slot_base", "clamp", "last_group", "odd_pair", "kv_end", "first_query", "parts"])
+], ids=["pad", "slot_base", "clamp", "last_group", "odd_pair", "kv_end", "key_parts", "join_tile", "first_query", "parts"])
 def test_planted_mistakes_are_found(tmp_path, header, old, new):
     inc = tmp_path / "inc"
     inc.mkdir()
@@ -123,6 +126,16 @@ def test_the_binding_packs_the_header_s_structures():
 def test_nothing_to_do():
     empty = dict(Tq=0, Q=rows(data=0), O=rows(data=0), dO=rows(data=0), dQ=rows(data=0))
     assert calls(empty | dict(Tk=0, K=rows(data=0), V=rows(data=0), dK=rows(data=0), dV=rows(data=0), ws=None)) == (0, 0)
+
+
+def test_forward_workspace_sizes():
+    size = fa.fwd_packed_workspace_size
+    assert size(1, 100, 3, 2, 64) == 0 and size(1, 100, 4, 2, 96) == 0 and size(0, 1, 1, 1, 64) == 0 and size(1, 0, 1, 1, 64) == 0
+    assert size(4, 8192, 32, 8, 128) == 0                     # enough query tiles: the keys stay whole
+    one = 100 * 4 * (128 + 2) * 4                             # a part: unnormalised O, maximum and sum
+    assert size(1, 100, 4, 2, 128) >= 2 * one
+    for over in (dict(ws=None), dict(ws=FAKE + 128), dict(wn=1000)):
+        assert calls(dict(Tk=5000) | over)[0] == 4
 
 
 def test_workspace_sizes():
