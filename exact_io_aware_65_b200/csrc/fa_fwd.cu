@@ -59,8 +59,8 @@ constexpr int RING = 4;              // depth of the item ring the producer fill
 // items gridDim.x, gridDim.x + 1, ... from a counter.  Each launch takes one
 // of SCHED_SLOTS counters (in turn, on the host), and the last CTA to stop
 // claiming puts it back to zero.  Launches that run at the same time (other
-// streams) use other slots, so at most SCHED_SLOTS forward launches may be
-// in flight at once.
+// streams) use other slots, so at most half of SCHED_SLOTS forward launches
+// may be in flight at once (the other half is for captured ones).
 constexpr uint32_t SCHED_SLOTS = 4096;
 __device__ uint32_t g_claim[SCHED_SLOTS];  // dynamic claims so far
 __device__ uint32_t g_done[SCHED_SLOTS];   // CTAs that stopped claiming
@@ -900,10 +900,15 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
   }
 }
 
-// The counter slot of the next launch.
-static uint32_t next_slot() {
-  static std::atomic<uint32_t> next{0};
-  return next.fetch_add(1u, std::memory_order_relaxed) % SCHED_SLOTS;
+// The counter slot of the next launch on `s`.  A captured launch keeps its slot
+// for as long as its graph lives, so it takes one from a half of its own: a
+// graph and launches outside it, on another stream, then never meet on a slot.
+static uint32_t next_slot(cudaStream_t s) {
+  static std::atomic<uint32_t> next[2];
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  const bool captured = cudaStreamIsCapturing(s, &st) == cudaSuccess && st != cudaStreamCaptureStatusNone;
+  constexpr uint32_t HALF = SCHED_SLOTS / 2;
+  return (captured ? HALF : 0u) + next[captured].fetch_add(1u, std::memory_order_relaxed) % HALF;
 }
 
 }  // namespace fwd
@@ -939,7 +944,7 @@ fa_status launch_fwd(const Problem& pr, const void* Q, const void* K, const void
   p.LSE = LSE;
   p.timeout_ns = wait_timeout_ns();
   p.status = st;
-  p.slot = fwd::next_slot();
+  p.slot = fwd::next_slot(s);
   const int npipe = dual ? 2 : 1;
   const int want = (p.n_items + npipe - 1) / npipe;  // CTAs that get a first item in every pipeline
   const int grid = want < num_sms() ? want : num_sms();
@@ -1022,7 +1027,7 @@ fa_status launch_fwd_packed(const PackedProblem& pr, const Rows& Q, const Rows& 
   p.LSE = LSE;
   p.timeout_ns = wait_timeout_ns();
   p.status = st;
-  p.slot = fwd::next_slot();
+  p.slot = fwd::next_slot(s);
   const int npipe = dual ? 2 : 1;
   const int want = (p.n_items + npipe - 1) / npipe;
   const int grid = want < num_sms() ? want : num_sms();
