@@ -900,15 +900,10 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
   }
 }
 
-// The counter slot of the next launch on `s`.  A captured launch keeps its slot
-// for as long as its graph lives, so it takes one from a half of its own: a
-// graph and launches outside it, on another stream, then never meet on a slot.
+// The counter slot of the next launch on `s`.
 static uint32_t next_slot(cudaStream_t s) {
-  static std::atomic<uint32_t> next[2];
-  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-  const bool captured = cudaStreamIsCapturing(s, &st) == cudaSuccess && st != cudaStreamCaptureStatusNone;
-  constexpr uint32_t HALF = SCHED_SLOTS / 2;
-  return (captured ? HALF : 0u) + next[captured].fetch_add(1u, std::memory_order_relaxed) % HALF;
+  static SlotTurn turn;
+  return turn.take(s, SCHED_SLOTS);
 }
 
 }  // namespace fwd

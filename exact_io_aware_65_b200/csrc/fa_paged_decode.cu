@@ -28,9 +28,10 @@
 // leaves fp16 room.
 // At the end of a unit the eight warps join their (O, m, l) in shared memory;
 // a unit that lies in one CTA is finished there, a part of one goes to the
-// workspace.
-// Kernel 2 (join): joins a unit's parts in CTA order (the same bits each run).
-// Kernel 3 (weights), on request: P = 2^(s - LSE log2 e) from the scores that
+// workspace, and the CTA that brings a unit's last part joins its parts, in their
+// order (the same bits each run): a second kernel for that cost 4 us more (one
+// sequence of 777 keys, 32 over 8 heads: JOIN2_US against JOIN1_US).
+// Kernel 2 (weights), on request: P = 2^(s - LSE log2 e) from the scores that
 // kernel 1 left in the workspace, summed over the group in head order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,6 +48,13 @@ namespace paged {
 
 constexpr int ROWS = 16;  // query heads of a unit, at most: 8 in a tile, NB tiles
 constexpr int THREADS = WARPS * 32;
+// Counters of the parts that have come, one a CTA that a divided unit begins in;
+// the CTA that joins a unit puts its counter back to zero.  Each launch takes one
+// of JOIN_SLOTS rows of them: half as many launches may be in flight at once.
+constexpr uint32_t JOIN_SLOTS = 2048;
+constexpr int MAX_GRID = 160;
+__device__ uint32_t g_came[JOIN_SLOTS][MAX_GRID];
+
 constexpr float SLACK = 8.0f;  // log2 units a score may lie above the reference maximum
 constexpr int MAX_BATCH = 4096;                 // sequences per launch (prefix of their blocks in shared memory)
 constexpr float LN2 = 0.69314718055994530942f;
@@ -65,7 +73,7 @@ struct DecodeParams {
   float sl2;                // scale * log2(e)
   float* part;              // [2 grid][ROWS][D] unnormalised O
   float2* ml;               // [2 grid][ROWS] (m, l)
-  int4* desc;               // [grid] (sequence, head unit, first part, parts) of the unit a CTA begins and does not end
+  uint32_t slot;            // row of g_came
   float* scores;            // [B, Hq, pitch] scaled log2 scores, or nullptr
   long long pitch;
   __nv_bfloat16* O;         // [B, Hq, D]
@@ -137,6 +145,8 @@ struct DCfg {
   static constexpr int UNIT = STEP * ROWB;
   static constexpr int QPITCH = 2 * D + 16;
   static constexpr int JPITCH = D + 4;
+  // (also the parts' (m, l) of a divided unit, and the sequences' prefix)
+  static_assert(MAX_GRID * R * 8 <= WARPS * R * JPITCH * 4, "shared memory for the join");
   static constexpr int JOIN_BYTES = WARPS * R * JPITCH * 4 > MAX_BATCH * 4 ? WARPS * R * JPITCH * 4 : MAX_BATCH * 4;
   static constexpr int FIT = (224 * 1024 - R * QPITCH - JOIN_BYTES) / (WARPS * UNIT);
   // Units of a ring: an odd number, so that a step frees the places of the K and
@@ -158,7 +168,7 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
   float* join = reinterpret_cast<float*>(sQ + R * C::QPITCH);  // the prefix at the start
   __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS], sm_sl2[ROWS];
   __shared__ int warp_sum[WARPS];
-  __shared__ int start_b, end_b;
+  __shared__ int start_b, end_b, join_c0, join_n;
   __shared__ long long sh_total;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -210,7 +220,6 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
       reinterpret_cast<uint4*>(p.O + (long long)b * p.Hq * D)[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = tid; i < p.Hq; i += THREADS) p.LSE[(long long)b * p.Hq + i] = -INFINITY;
   }
-  if (tid == 0) p.desc[cta] = make_int4(-1, 0, 0, 0);
   __syncthreads();  // prefix has been read
   if (w.at >= w.end) return;
 
@@ -589,8 +598,8 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
         }
       }
     __syncthreads();
+    const bool whole = nseg == w.nblk;
     {
-      const bool whole = nseg == w.nblk;
       const float vs = E4M3 ? __ldg(p.c.v_scale + hk) : 1.0f;
       const int part = part_slot(cta, begin, unit_begin);
       for (int k = tid; k < heads * (D / 4); k += THREADS) {
@@ -618,10 +627,49 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
           if (col == 0) p.ml[(long long)part * ROWS + h] = make_float2(M, L);
         }
       }
-      // the unit begins here and goes on: the join kernel's block `cta` joins it
-      if (tid == 0 && !whole && w.blk == 0) {
-        const int last = owner(total, grid, unit_begin + w.nblk - 1);
-        p.desc[cta] = make_int4(b, w.hu, part, last - cta + 1);
+    }
+    if (!whole) {
+      // The CTA whose part of the unit comes last joins them all.
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int c0 = owner(total, grid, unit_begin), n = owner(total, grid, unit_begin + w.nblk - 1) - c0 + 1;
+        const bool last = atomicAdd(&g_came[p.slot][c0], 1u) == (uint32_t)n - 1;
+        if (last) g_came[p.slot][c0] = 0u;
+        join_c0 = c0;
+        join_n = last ? n : 0;
+      }
+      __syncthreads();
+      if (join_n > 0) {
+        __threadfence();
+        const int c0 = join_c0, n = join_n;
+        // in CTAs after c0 the unit comes first: slot 2 c
+        const int first = part_slot(c0, share(total, grid, c0), unit_begin);
+        auto slot_of = [&](int i) { return (long long)(i ? 2 * (c0 + i) : first) * ROWS; };
+        float2* ml = reinterpret_cast<float2*>(join);  // [n][R]: (m, l) of the parts
+        for (int k = tid; k < n * R; k += THREADS) ml[k] = __ldcg(p.ml + slot_of(k / R) + k % R);
+        __syncthreads();
+        for (int k = tid; k < heads * (D / 4); k += THREADS) {
+          const int h = k / (D / 4), col = k % (D / 4) * 4;
+          float M = -INFINITY;
+          for (int i = 0; i < n; ++i) M = fmaxf(M, ml[i * R + h].x);
+          const float ref = M == -INFINITY ? 0.0f : M;
+          float L = 0.0f;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int i = 0; i < n; ++i) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + (slot_of(i) + h) * D + col));
+            const float2 z = ml[i * R + h];
+            const float f = ex2_approx(z.x - ref);
+            L = fmaf(z.y, f, L);
+            x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+          }
+          const float inv = L > 0.0f ? 1.0f / L : L == 0.0f ? 0.0f : L;
+          *reinterpret_cast<uint2*>(p.O + (q_first + h) * D + col) =
+              make_uint2(pack2<false>(x.x * inv, x.y * inv), pack2<false>(x.z * inv, x.w * inv));
+          if (col == 0) p.LSE[q_first + h] = (M + log2f(L)) * LN2;
+        }
+        __syncthreads();  // ml, which the next unit's join overwrites
       }
     }
     // (sm_m, sm_l and the joined rows are written again only after the next
@@ -631,43 +679,6 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
     if (w.blk == w.nblk) next_unit(work, w);
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-}
-
-// Block (c, r): row r of the unit that begins in CTA c and ends in another.
-template <int D>
-__global__ void __launch_bounds__(D) join_kernel(const DecodeParams p, int rows) {
-  const int c0 = blockIdx.x / rows, r = blockIdx.x % rows, col = threadIdx.x;
-  const int4 u = p.desc[c0];
-  if (u.x < 0) return;
-  const int hk = u.y / p.HB, row0 = (u.y % p.HB) * p.R;
-  if (r >= min(p.R, p.G - row0)) return;
-  // in CTAs after c0 the unit comes first: slot 2 c
-  auto part_row = [&](int i) { return (long long)(i ? 2 * (c0 + i) : u.z) * ROWS + r; };
-  // every warp finds the maximum and the sum, a part a lane; 2^(m - M) of the
-  // parts to shared memory
-  __shared__ float factor[1024];  // (a part a CTA, a CTA an SM)
-  const int lane = col & 31;
-  float M = -INFINITY;
-  for (int i = lane; i < u.w; i += 32) M = fmaxf(M, p.ml[part_row(i)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float ref = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f;
-  for (int i = lane; i < u.w; i += 32) {
-    const float2 ml = p.ml[part_row(i)];
-    const float f = ex2_approx(ml.x - ref);
-    L = fmaf(ml.y, f, L);
-    if (col < 32) factor[i] = f;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  __syncthreads();
-  float acc = 0.0f;
-#pragma unroll 8
-  for (int i = 0; i < u.w; ++i) acc = fmaf(p.part[part_row(i) * D + col], factor[i], acc);
-  const long long row = (long long)u.x * p.Hq + hk * p.G + row0 + r;
-  p.O[row * D + col] = __float2bfloat16(L == 0.0f ? 0.0f : acc / L);
-  if (col == 0) p.LSE[row] = (M + log2f(L)) * LN2;
 }
 
 // A[b, hk, j] (+)= sum over the group of 2^(s_j - LSE log2 e): four keys a
@@ -699,20 +710,25 @@ __global__ void __launch_bounds__(W_THREADS) weights_kernel(const DecodeParams p
   }
 }
 
-// One CTA per SM, at most as many as the join kernel keeps factors for.
-static int decode_grid() { return num_sms() < 1024 ? num_sms() : 1024; }
+// The counters of the next launch on `s`, of whatever type.
+static uint32_t next_slot(cudaStream_t s) {
+  static SlotTurn turn;
+  return turn.take(s, JOIN_SLOTS);
+}
+
+// One CTA per SM, at most as many as there are counters.
+static int decode_grid() { return num_sms() < MAX_GRID ? num_sms() : MAX_GRID; }
 
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct DecodeLayout {
-  size_t part, ml, desc, scores, total;
+  size_t part, ml, scores, total;
 };
 static DecodeLayout layout(int B, int Hq, int d, long long cap, bool weights, int grid) {
   DecodeLayout w;
   w.part = 0;
   w.ml = align256((size_t)2 * grid * ROWS * d * sizeof(float));
-  w.desc = w.ml + align256((size_t)2 * grid * ROWS * sizeof(float2));
-  w.scores = w.desc + align256((size_t)grid * sizeof(int4));
+  w.scores = w.ml + align256((size_t)2 * grid * ROWS * sizeof(float2));
   w.total = w.scores + (weights ? align256((size_t)B * Hq * ((cap + STEP - 1) / STEP * STEP) * sizeof(float)) : 0);
   return w;
 }
@@ -745,9 +761,8 @@ static fa_status launch_d(paged::DecodeParams p, int B, const PagedDecode& a, in
     p.O = O + (long long)b0 * p.Hq * D;
     p.LSE = LSE + (long long)b0 * p.Hq;
     if (scores) p.scores = scores + (long long)b0 * p.Hq * p.pitch;
+    p.slot = next_slot(s);
     if (!launch(kern, (unsigned)grid, THREADS, smem, s, p)) return FA_ERR_CUDA;
-    const int rows = p.G < p.R ? p.G : p.R;
-    if (!p.whole && !launch(join_kernel<D>, (unsigned)(grid * rows), D, 0, s, p, rows)) return FA_ERR_CUDA;
     if (scores) {
       long long chunks = (p.pitch + 4 * W_THREADS - 1) / (4 * W_THREADS);  // four keys a thread
       if (chunks > 64) chunks = 64;
@@ -787,7 +802,6 @@ fa_status launch_paged_decode(const PagedCache& c, const PagedDecode& a, cudaStr
   p.sl2 = a.scale_log2;
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
-  p.desc = reinterpret_cast<int4*>(ws + w.desc);
   p.scores = a.W ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
   p.pitch = (cap + paged::STEP - 1) / paged::STEP * paged::STEP;
   p.O = static_cast<__nv_bfloat16*>(a.O);

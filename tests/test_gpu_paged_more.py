@@ -76,3 +76,46 @@ def test_evict_where_keys_share_their_upper_bits(kind):
     for b in range(2):
         for h in range(2):
             assert kept[b, h].tolist() == ref.evict(w[b, h].tolist(), n - 7 * b, budget, recent)
+
+
+def test_decode_calls_at_once_and_many_after_another():
+    # divided units on two streams and in a graph, each with buffers of its own;
+    # then more calls than there are rows of counters
+    c = ref.dev(ref.make_cache([5000, 700, 3100], 2, 128, 16, seed=7, poison=False))
+    e = ref.dev(ref.make_cache([9000], 2, 64, 64, True, seed=8, poison=False))
+    Q, R = randn(3, 8, 128, seed=9).cuda(), randn(1, 20, 64, seed=10).cuda()
+    f = lambda **k: fa.paged_decode(Q, c["kc"], c["vc"], c["table"], c["lens"], **k)
+    h = lambda **k: fa.paged_decode(R, e["kc"], e["vc"], e["table"], e["lens"], k_scale=e["ks"], v_scale=e["vs"], **k)
+    want = [t.clone() for t in (*f(), *h())]
+    bufs = [torch.empty_like(t) for t in want]
+    ws = [torch.empty(fa.paged_decode_workspace_size(*a), dtype=torch.uint8, device="cuda")
+          for a in ((3, 8, 2, 128, c["table"].shape[1] * 16), (1, 20, 2, 64, e["table"].shape[1] * 64))]
+
+    def step():
+        f(O=bufs[0], LSE=bufs[1], workspace=ws[0])
+        h(O=bufs[2], LSE=bufs[3], workspace=ws[1])
+
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    with torch.cuda.stream(streams[2]):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    got = []
+    for _ in range(20):
+        for t in (*bufs, *ws):
+            t.fill_(1)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(streams[2]):
+            graph.replay()
+        for s in streams[:2]:
+            got += [(f(stream=s), 0), (h(stream=s), 2)]
+        torch.cuda.synchronize()
+        for t, w in zip(bufs, want):
+            assert torch.equal(t, w)
+    for (O, L), i in got:
+        assert torch.equal(O, want[i]) and torch.equal(L, want[i + 1])
+    for _ in range(2200):
+        O, L = h()
+    assert torch.equal(O, want[2]) and torch.equal(L, want[3]) and fa.device_status() == 0
