@@ -30,7 +30,7 @@
 // a unit that lies in one CTA is finished there, a part of one goes to the
 // workspace, and the CTA that brings a unit's last part joins its parts, in their
 // order (the same bits each run): a second kernel for that cost 4 us more (one
-// sequence of 777 keys, 32 over 8 heads: JOIN2_US against JOIN1_US).
+// sequence of 777 keys, 32 over 8 heads: 14.4 us against 12.4).
 // Kernel 2 (weights), on request: P = 2^(s - LSE log2 e) from the scores that
 // kernel 1 left in the workspace, summed over the group in head order.
 #include <cuda_bf16.h>
@@ -169,16 +169,37 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
   __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS], sm_sl2[ROWS];
   __shared__ int warp_sum[WARPS];
   __shared__ int start_b, end_b, join_c0, join_n;
-  __shared__ long long sh_total;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int HU = p.Hkv * p.HB, cta = blockIdx.x;
 
-  // ---- this CTA's blocks.  prefix[b]: blocks of a head unit in the sequences
-  // up to b.
-  int* prefix = reinterpret_cast<int*>(join);
-  {
+  // ---- this CTA's blocks
+  const Work work{&p.c, p.lens, p.B, HU};
+  Walk w;
+  long long total;  // blocks of all units
+  int grid;         // CTAs with blocks (with fewer blocks than CTAs the first `total` take one each, so that no CTA
+                    // between a unit's first and last is without a part)
+  if (p.B <= 32) {
+    // every warp for itself: a lane a sequence
+    const int mine = lane < p.B ? blocks_of(clamp_len(p.c, __ldg(p.lens + lane))) : 0;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    total = (long long)__shfl_sync(0xffffffffu, upto, 31) * HU;
+    grid = (int)min((long long)gridDim.x, total);
+    auto start = [&](int c) {
+      const unsigned past = __ballot_sync(0xffffffffu, c < grid && (long long)upto * HU > share(total, grid, c));
+      const int b = past ? __ffs(past) - 1 : 0;
+      return start_walk_at(work, __shfl_sync(0xffffffffu, upto - mine, b), b, total, grid, c);
+    };
+    w = start(cta);
+    if (p.whole) w = whole_units(work, w, start(cta + 1), grid, cta);
+  } else {
+    int* prefix = reinterpret_cast<int*>(join);  // [b]: blocks of a head unit in the sequences up to b
     int carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
       const int b = b0 + tid;
@@ -196,22 +217,17 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
       for (int v = 0; v < WARPS; ++v) carry += warp_sum[v];
       __syncthreads();
     }
+    total = (long long)carry * HU;
+    grid = (int)min((long long)gridDim.x, total);
     if (tid == 0) {
-      const long long all = (long long)carry * HU;
-      const int n = (int)min((long long)gridDim.x, all);
-      sh_total = all;
-      start_b = cta < n ? sequence_of(prefix, p.B, HU, share(all, n, cta)) : 0;
-      end_b = p.whole && cta + 1 < n ? sequence_of(prefix, p.B, HU, share(all, n, cta + 1)) : 0;
+      start_b = cta < grid ? sequence_of(prefix, p.B, HU, share(total, grid, cta)) : 0;
+      end_b = p.whole && cta + 1 < grid ? sequence_of(prefix, p.B, HU, share(total, grid, cta + 1)) : 0;
     }
     __syncthreads();
+    w = start_walk(work, prefix, start_b, total, grid, cta);
+    if (p.whole) w = whole_units(work, w, start_walk(work, prefix, end_b, total, grid, cta + 1), grid, cta);
+    __syncthreads();  // prefix has been read
   }
-  // (with fewer blocks than CTAs the first `total` CTAs take one each, so that
-  // no CTA between a unit's first and last is without a part)
-  const long long total = sh_total;
-  const int grid = (int)min((long long)gridDim.x, total);
-  const Work work{&p.c, p.lens, p.B, HU};
-  Walk w = start_walk(work, prefix, start_b, total, grid, cta);
-  if (p.whole) w = whole_units(work, prefix, w, end_b, total, grid, cta);
   const long long begin = w.at;
   // sequences without keys: nothing else writes their rows
   for (int b = cta; b < p.B; b += gridDim.x) {
@@ -220,7 +236,6 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
       reinterpret_cast<uint4*>(p.O + (long long)b * p.Hq * D)[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = tid; i < p.Hq; i += THREADS) p.LSE[(long long)b * p.Hq + i] = -INFINITY;
   }
-  __syncthreads();  // prefix has been read
   if (w.at >= w.end) return;
 
   // ---- the copies run up to NU units ahead of the products (K, V, K, V, ...),
@@ -794,9 +809,9 @@ fa_status launch_paged_decode(const PagedCache& c, const PagedDecode& a, cudaStr
   p.HB = (p.G + p.R - 1) / p.R;
   p.page = paged::make_divider(c.page_size);
   // Short caches: a unit's few blocks one after the other take less time than
-  // their parts' join and its launch (16 sequences of 500 keys, 32 over 8 heads of
-  // 128: 11.0 against 15.0 us; one of 500: 10.4 against 10.9; one of 777, in seven
-  // blocks, would take 13.3 against 12.3).
+  // their parts' join (16 sequences of 500 keys, 32 over 8 heads of 128: 10.2
+  // against 16.5 us; 64 of 250, 16 heads: 35.0 against 42.1; one of 500: 9.9
+  // against 9.4).
   p.whole = cap <= 4 * paged::BLOCK;
   p.wide = ((c.num_pages - 1) * c.page_stride + (c.page_size - 1) * c.row_stride) * c.elem >= (1ll << 36);
   p.sl2 = a.scale_log2;

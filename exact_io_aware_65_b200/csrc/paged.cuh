@@ -76,11 +76,16 @@ constexpr int STEP = 16;             // keys a warp handles at a time
 constexpr int BLOCK = WARPS * STEP;  // keys of one block
 
 __host__ __device__ __forceinline__ int blocks_of(int len) { return (len + BLOCK - 1) / BLOCK; }
-__host__ __device__ __forceinline__ long long share(long long total, int grid, int c) { return total * c / grid; }
+// a / b for a >= 0, b > 0: in 32 bits where they do (a 64-bit division takes about
+// a hundred instructions).
+__host__ __device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__host__ __device__ __forceinline__ long long share(long long total, int grid, int c) { return quotient(total * c, grid); }
 
 // The CTA that holds block x: the largest c with share(c) <= x.
 __host__ __device__ __forceinline__ int owner(long long total, int grid, long long x) {
-  int c = (int)(x * grid / total);
+  int c = (int)quotient(x * grid, total);
   while (c + 1 < grid && share(total, grid, c + 1) <= x) ++c;
   while (c > 0 && share(total, grid, c) > x) --c;
   return c;
@@ -112,10 +117,10 @@ __host__ __device__ __forceinline__ void enter_sequence(const Work& k, Walk& w) 
   w.nblk = blocks_of(w.len);
 }
 
-// The start of CTA `cta` of `grid` <= total; prefix[b]: blocks of one head unit
-// in sequences 0 .. b.
-__host__ __device__ __forceinline__ Walk start_walk(const Work& k, const int* prefix, int b, long long total, int grid,
-                                                    int cta) {
+// The start of CTA `cta` of `grid` <= total, in sequence b; before: blocks of one
+// head unit in the sequences before it.
+__host__ __device__ __forceinline__ Walk start_walk_at(const Work& k, int before, int b, long long total, int grid,
+                                                       int cta) {
   Walk w;
   w.at = cta < grid ? share(total, grid, cta) : total;
   w.end = cta < grid ? share(total, grid, cta + 1) : total;
@@ -123,11 +128,16 @@ __host__ __device__ __forceinline__ Walk start_walk(const Work& k, const int* pr
   w.hu = w.blk = w.nblk = w.len = 0;
   if (w.at < w.end) {
     enter_sequence(k, w);
-    const long long into = w.at - (b > 0 ? (long long)prefix[b - 1] * k.HU : 0);
-    w.hu = (int)(into / w.nblk);
-    w.blk = (int)(into % w.nblk);
+    const long long into = w.at - (long long)before * k.HU;
+    w.hu = (int)quotient(into, w.nblk);
+    w.blk = (int)(into - (long long)w.hu * w.nblk);
   }
   return w;
+}
+// The same from prefix[b], the blocks of one head unit in sequences 0 .. b.
+__host__ __device__ __forceinline__ Walk start_walk(const Work& k, const int* prefix, int b, long long total, int grid,
+                                                    int cta) {
+  return start_walk_at(k, b > 0 ? prefix[b - 1] : 0, b, total, grid, cta);
 }
 
 // The sequence that holds block x: the first b with prefix[b] * HU > x.
@@ -154,12 +164,11 @@ __host__ __device__ __forceinline__ void next_unit(const Work& k, Walk& w) {
 }
 
 // Whole units only: a CTA takes the units that begin in its share.  w: its walk;
-// next_b: the sequence that holds the first block of the next CTA's share.
+// next: the walk that the next CTA starts with.
 __host__ __device__ __forceinline__ long long unit_boundary(const Walk& w) { return w.blk > 0 ? w.at + (w.nblk - w.blk) : w.at; }
-__host__ __device__ __forceinline__ Walk whole_units(const Work& k, const int* prefix, Walk w, int next_b, long long total,
-                                                     int grid, int cta) {
+__host__ __device__ __forceinline__ Walk whole_units(const Work& k, Walk w, const Walk& next, int grid, int cta) {
   if (w.at >= w.end) return w;
-  if (cta + 1 < grid) w.end = unit_boundary(start_walk(k, prefix, next_b, total, grid, cta + 1));
+  if (cta + 1 < grid) w.end = unit_boundary(next);
   if (w.blk > 0) {
     w.at = unit_boundary(w);
     next_unit(k, w);

@@ -30,7 +30,8 @@ static int check(const std::vector<int>& lens, int HU, int gpu) {
   for (int cta = 0; cta < gpu; ++cta) {
     const int b0 = cta < grid ? sequence_of(prefix.data(), B, HU, share(total, grid, cta)) : 0;
     const int b1 = cta + 1 < grid ? sequence_of(prefix.data(), B, HU, share(total, grid, cta + 1)) : 0;
-    Walk w = whole_units(k, prefix.data(), start_walk(k, prefix.data(), b0, total, grid, cta), b1, total, grid, cta);
+    Walk w = whole_units(k, start_walk(k, prefix.data(), b0, total, grid, cta),
+                         start_walk(k, prefix.data(), b1, total, grid, cta + 1), grid, cta);
     while (w.at < w.end) {
       if (w.blk != 0 || w.nblk <= 0 || w.at + w.nblk > w.end || !seen.insert({w.b, w.hu}).second) {
         printf("MISMATCH cta %d of %d: sequence %d unit %d block %d of %d, at %lld, end %lld\n", cta, gpu, w.b, w.hu, w.blk,
