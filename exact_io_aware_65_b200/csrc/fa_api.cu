@@ -518,7 +518,7 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_CUDA: return "CUDA error";
     case FA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case FA_ERR_TIMEOUT: return "a bounded device-side wait timed out";
-    case FA_ERR_BOUNDS: return "a device-side index check failed (debug build)";
+    case FA_ERR_BOUNDS: return "an index lay outside its buffer, and the access was skipped";
   }
   return "unknown status";
 }

@@ -6,8 +6,11 @@
 // slot position % page_size of page table[b, position / page_size]: a copy in
 // bf16, or the nearest 8-bit value (4 exponent bits, 3 of fraction) of
 // x / scale, ties to even, magnitudes above the type's largest (448) held
-// there.  Bound by HBM (prompts) or by the chain of dependent loads that finds
-// the row (single tokens).
+// there.  Bound by the conversion's instructions (8476 tokens of 8 heads of 128
+// into 8 bits: 14.4 us, of which HBM needs 8) or by the chain of dependent loads
+// that finds the row (a step of 64 sequences: 3 us, most of it the launch).
+// Evict.  Bound by the chain of its passes (small caches: 9 us) or by HBM (eight
+// caches of 7000-8192 rows cut to 2048: 14 us to select, 27 to move 137 MB).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math.h>
