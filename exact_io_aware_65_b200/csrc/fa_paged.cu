@@ -249,6 +249,14 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, in
   for (int r = r0 + threadIdx.x; r < end; r += blockDim.x) wo[r] = __ldg(w + kept[r]);
 }
 
+// The sum of what the warps before this one put into v[32].
+__device__ __forceinline__ int sum_before(const int* v, int warp, int lane) {
+  int x = lane < warp ? v[lane] : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
 // The positions that stay; the CTA's (sequence, head) in p.kept, and how many.
 __device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys) {
   __shared__ uint32_t hist[SEL_BINS];
@@ -329,7 +337,7 @@ __device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys)
     before -= c0 + c1;
     __syncthreads();
     hist[top] = hist[top - 1] = 0u;  // for the next digits
-    for (int v = 0; v < warp; ++v) before += (uint32_t)above_w[v];
+    before += (uint32_t)sum_before(above_w, warp, lane);
     if (before < (uint32_t)need && before + c0 + c1 >= (uint32_t)need) {  // one thread
       const bool second = before + c0 < (uint32_t)need;
       sh_digit = (uint32_t)(second ? top - 1 : top);
@@ -357,12 +365,8 @@ __device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys)
     tie_w[warp] = ties;
   }
   __syncthreads();
-  int at = 0, tie_at = 0;  // what the warps before keep, and how many ties they have
-  for (int v = 0; v < warp; ++v) {
-    at += above_w[v];
-    tie_at += tie_w[v];
-  }
-  at += min(tie_at, need);
+  int tie_at = sum_before(tie_w, warp, lane);                     // ties of the warps before,
+  int at = sum_before(above_w, warp, lane) + min(tie_at, need);  // and what they keep
   const unsigned before_me = (1u << lane) - 1u;
   for (int i = i0 + lane; i - lane < i1; i += 32) {
     const uint32_t k = i < i1 ? key_at(i) >> shift : 0u;
