@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import warnings
 
 import torch
 
@@ -124,10 +125,14 @@ def lib() -> ctypes.CDLL:
             f.argtypes = args
         _lib = L
         if os.path.exists(os.path.join(_HERE, "_binding.so")):
-            from . import _binding
+            try:
+                from . import _binding
 
-            _binding.use(L._handle)
-            _fast = _binding
+                _binding.use(L._handle)
+                _fast = _binding
+            except ImportError as e:  # built against another torch
+                warnings.warn(f"_binding.so does not load ({e}); calls go through ctypes. Rebuild it with "
+                              "`python -m exact_io_aware_65_b200.build`")
     return _lib
 
 

@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const PackedArgs a) {
       float l2 = INFINITY;  // rows before the sequence, and rows that saw no key: P = 0
       if (n >= 0 && FA_IN_BOUNDS(a.status, (size_t)h * a.pk.Tq + s.sq + n, 1, (size_t)a.pk.Hq * a.pk.Tq)) {
         const float lse = a.LSE[(size_t)h * a.pk.Tq + s.sq + n];
-        if (lse > -INFINITY) l2 = lse * LOG2E;
+        if (lse != -INFINITY) l2 = lse * LOG2E;  // (a NaN of the forward's stays one)
       }
       a.L2w[row] = -l2;
     }

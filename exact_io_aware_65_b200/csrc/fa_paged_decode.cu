@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
   float* join = reinterpret_cast<float*>(sQ + R * C::QPITCH);  // the prefix at the start
   __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS], sm_sl2[ROWS];
   __shared__ int warp_sum[WARPS];
-  __shared__ int start_b, end_b, join_c0, join_n;
+  __shared__ int start_b, end_b, join_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -647,40 +647,58 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
       }
     }
     if (!whole) {
-      // The CTA whose part of the unit comes last joins them all.
-      __threadfence();
+      // The CTA whose part of the unit comes last joins them all.  (A CTA's barrier
+      // orders its threads' stores before thread 0's fence, and its fence before
+      // their loads.)
+      const int c0 = owner(total, grid, unit_begin), n = owner(total, grid, unit_begin + w.nblk - 1) - c0 + 1;
       __syncthreads();
       if (tid == 0) {
-        const int c0 = owner(total, grid, unit_begin), n = owner(total, grid, unit_begin + w.nblk - 1) - c0 + 1;
+        __threadfence();
         const bool last = atomicAdd(&g_came[p.slot][c0], 1u) == (uint32_t)n - 1;
-        if (last) g_came[p.slot][c0] = 0u;
-        join_c0 = c0;
-        join_n = last ? n : 0;
+        if (last) {
+          g_came[p.slot][c0] = 0u;
+          __threadfence();
+        }
+        join_last = last;
       }
       __syncthreads();
-      if (join_n > 0) {
-        __threadfence();
-        const int c0 = join_c0, n = join_n;
+      if (join_last) {
         // in CTAs after c0 the unit comes first: slot 2 c
         const int first = part_slot(c0, share(total, grid, c0), unit_begin);
         auto slot_of = [&](int i) { return (long long)(i ? 2 * (c0 + i) : first) * ROWS; };
         float2* ml = reinterpret_cast<float2*>(join);  // [n][R]: (m, l) of the parts
         for (int k = tid; k < n * R; k += THREADS) ml[k] = __ldcg(p.ml + slot_of(k / R) + k % R);
-        __syncthreads();
-        for (int k = tid; k < heads * (D / 4); k += THREADS) {
-          const int h = k / (D / 4), col = k % (D / 4) * 4;
+        for (int k0 = 0; k0 < heads * (D / 4); k0 += THREADS) {
+          const int k = k0 + tid, h = k / (D / 4), col = k % (D / 4) * 4;
+          const bool mine = h < heads;
+          auto load = [&](int i) {
+            return mine && i < n ? __ldcg(reinterpret_cast<const float4*>(p.part + (slot_of(i) + h) * D + col))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+          };
+          constexpr int U = 8;  // parts on their way while the maxima are
+          float4 y[U];
+#pragma unroll
+          for (int i = 0; i < U; ++i) y[i] = load(i);
+          __syncthreads();
+          if (!mine) continue;
           float M = -INFINITY;
           for (int i = 0; i < n; ++i) M = fmaxf(M, ml[i * R + h].x);
           const float ref = M == -INFINITY ? 0.0f : M;
           float L = 0.0f;
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int i = 0; i < n; ++i) {
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + (slot_of(i) + h) * D + col));
-            const float2 z = ml[i * R + h];
-            const float f = ex2_approx(z.x - ref);
-            L = fmaf(z.y, f, L);
-            x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+          for (int i0 = 0; i0 < n; i0 += U) {
+            if (i0 > 0) {
+#pragma unroll
+              for (int i = 0; i < U; ++i) y[i] = load(i0 + i);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+              if (i0 + i >= n) break;
+              const float2 z = ml[(i0 + i) * R + h];
+              const float f = ex2_approx(z.x - ref);
+              L = fmaf(z.y, f, L);
+              x = make_float4(fmaf(y[i].x, f, x.x), fmaf(y[i].y, f, x.y), fmaf(y[i].z, f, x.z), fmaf(y[i].w, f, x.w));
+            }
           }
           const float inv = L > 0.0f ? 1.0f / L : L == 0.0f ? 0.0f : L;
           *reinterpret_cast<uint2*>(p.O + (q_first + h) * D + col) =

@@ -140,6 +140,19 @@ def test_values_that_are_not_seen_do_not_spread(d, more):
     assert torch.isfinite(O2[20, 0]).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_nan_that_is_seen_reaches_the_gradients(d):
+    n = [150, 90]
+    Q, K, V, dO, c, _ = batch(n, n, 4, 2, d, seed=12)
+    K[200, 1, 5] = math.nan  # row 50 of the second sequence, key head 1: seen by its queries from 50 on
+    O, L = fa.fwd_packed(Q, K, V, c, c, mask="causal")
+    assert torch.isnan(L[2:, 200:]).all() and torch.isfinite(L[:, :200]).all() and torch.isfinite(L[:2]).all()
+    dQ, dK, dV = fa.bwd_packed(Q, K, V, O, dO, L, c, c, mask="causal")
+    assert torch.isnan(dQ[200:, 2:]).all() and torch.isnan(dV[150:, 1]).all() and torch.isnan(dK[150:, 1]).all()
+    for g in (dQ[:150], dQ[:, :2], dK[:150], dK[:, 0], dV[:150], dV[:, 0]):
+        assert torch.isfinite(g).all()
+
+
 def test_starts_outside_the_tensors_are_held_to_them():
     Q, K, V, dO, _, _ = batch([300], [300], 4, 2, 64, seed=3)
     ok = run(Q, K, V, dO, i32([0, 100, 300]), i32([0, 100, 300]))
