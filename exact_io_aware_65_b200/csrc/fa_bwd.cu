@@ -212,11 +212,9 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const PackedArgs a) {
   const int lane = threadIdx.x & 31, sub = lane / LPR, li = lane % LPR;
   const int slot = blockIdx.x / a.pk.Hq, h = blockIdx.x % a.pk.Hq;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.sched = 0u;
-  const int b = pack::sequence_of_slot(a.pk, slot);
-  if (b < 0) return;
-  const pack::Seq s = pack::seq_at(a.pk, b);
-  const int i = slot - pack::slot_base(s.sq, b);
-  if (i >= pack::tiles(s.Lq)) return;  // a slot that no tile uses
+  const pack::Slot s = pack::find_slot(a.pk, slot);
+  const int i = s.tile;
+  if (i < 0) return;  // a slot that no tile uses
   if (threadIdx.x == 0) a.turn[blockIdx.x] = 0u;
   const int first = i * 128 - pack::pad(s.Lq);  // row of the sequence (negative: none)
 #pragma unroll
@@ -264,11 +262,9 @@ __global__ void __launch_bounds__(256) packed_convert_kernel(const PackedArgs a,
     constexpr int QUARTERS = D / 32;
     const int tile = blockIdx.x / QUARTERS;
     const int slot = tile / a.pk.Hq, h = tile % a.pk.Hq;
-    const int b = pack::sequence_of_slot(a.pk, slot);
-    if (b < 0) return;
-    const pack::Seq s = pack::seq_at(a.pk, b);
-    const int i = slot - pack::slot_base(s.sq, b);
-    if (i >= pack::tiles(s.Lq)) return;
+    const pack::Slot s = pack::find_slot(a.pk, slot);
+    const int i = s.tile;
+    if (i < 0) return;
     const int first = i * 128 - pack::pad(s.Lq);
     const float4* t = reinterpret_cast<const float4*>(a.dq_acc + (size_t)tile * 128 * D);
     const int eb = (blockIdx.x % QUARTERS) * 2 + threadIdx.x / 128, r = threadIdx.x % 128, n = first + r;
@@ -1292,18 +1288,32 @@ fa_status launch_bwd(const Problem& pr, const void* Q, const void* K, const void
   return launch_bwd_d<128>(pr, mQ, mK, mV, mdO, O, dO, LSE, dQ, dK, dV, workspace, s, st, stage);
 }
 
-// Parts that a key head's query heads are divided into, so that every SM gets
-// four items or more and the longest of them do not end last: a key head's items
-// are as many times longer as it has query heads.  Each part writes dK and dV in
-// fp32, and the last kernel adds them.
-static int packed_parts(const Pack& k) {
-  const long long items = (long long)(k.Tk / 128 + (k.B + 1) / 2) * k.Hkv;
-  const long long want = 4LL * num_sms();
-  if (k.G == 1 || items >= want || items == 0) return 1;
-  const long long n = (want + items - 1) / items;
-  if (n >= k.G) return k.G;
-  const int each = (int)((k.G + n - 1) / n);  // query heads of a part, at most
-  return (k.G + each - 1) / each;
+// Parts that a key head's query heads are divided into: more, shorter items fill
+// the GPU and end closer together, but each costs about five steps' time besides
+// its steps (its first loads and scores, its gradients' way out), and the parts'
+// fp32 dK and dV are written and read once more.  In units of a step (2.1 us),
+// with the lengths at their mean and a causal mask (whose longest items have
+// twice the mean's steps).  Three sequences of 1000, 24 over 8 heads of 64: 75 us
+// in one part, 93 in three; one of 6000, 8 over 1: 167 in eight, 208 in four.
+static int packed_parts(const Pack& k, int d) {
+  if (k.G == 1 || k.Tk == 0) return 1;
+  const float tiles = (float)k.Tq / 128.0f / (float)k.B + 0.5f;   // of a sequence's queries
+  const float items = ((float)k.Tk / 128.0f + 0.5f * (float)k.B) * (float)k.Hkv / (float)num_sms();  // an SM's
+  const float add = 24.0f * (float)k.Tk * (float)k.Hkv * (float)d / 5.5e6f / 2.1f;  // of a part's sums, at 5.5 TB/s
+  int best = 1;
+  float least = 0.0f;
+  for (int n = 1; n <= k.G && n <= 64; ++n) {
+    const int each = (k.G + n - 1) / n;  // query heads of a part, at most
+    if (n > 1 && (k.G + each - 1) / each != n) continue;  // fewer parts do the same
+    const float mean = (float)each * (tiles + 1.0f) * 0.5f, longest = (float)each * tiles;
+    const float whole = items * (float)n * (5.0f + mean) + 0.5f * longest;
+    const float cost = (whole > 5.0f + longest ? whole : 5.0f + longest) + (n > 1 ? add * (float)n : 0.0f);
+    if (n == 1 || cost < least) {
+      best = n;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 struct PackedWorkspace {
@@ -1314,7 +1324,7 @@ static PackedWorkspace packed_layout(const Pack& k, int d) {
   PackedWorkspace l;
   l.w = bwd::workspace_layout(k.Hq, (int)pack::slots(k.Tq, k.B) * 128, d);
   l.part_off = l.w.total;
-  const int parts = packed_parts(k);
+  const int parts = packed_parts(k, d);
   l.total = l.part_off + (parts > 1 ? bwd::align256((size_t)parts * 2 * k.Tk * k.Hkv * d * sizeof(float)) : 0);
   return l;
 }
@@ -1335,7 +1345,7 @@ static fa_status launch_bwd_packed_d(const PackedProblem& pr, const CUtensorMap&
   a.L2w = reinterpret_cast<float*>(ws + l.w.l2_off);
   a.sched = reinterpret_cast<uint32_t*>(ws + l.w.sched_off);
   a.turn = reinterpret_cast<uint32_t*>(ws + l.w.turn_off);
-  a.parts = packed_parts(k);
+  a.parts = packed_parts(k, D);
   float* part = a.parts > 1 ? reinterpret_cast<float*>(ws + l.part_off) : nullptr;
   a.part = part;
   a.scale = pr.scale;

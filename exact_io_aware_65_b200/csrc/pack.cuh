@@ -75,6 +75,33 @@ __device__ __forceinline__ int sequence_of_slot(const Pack& k, int slot) {
   return lo - 1;
 }
 
+// A slot's query rows and tile (-1: no tile uses the slot).  Warp-collective.
+struct Slot {
+  int sq, Lq, tile;
+};
+__device__ __forceinline__ Slot find_slot(const Pack& k, int slot) {
+  Slot s{0, 0, -1};
+  int b;
+  if (k.B <= 32) {  // a lane a sequence: no load waits for another
+    const int lane = threadIdx.x & 31;
+    const int from = min(max(__ldg(k.cu_q + min(lane, k.B)), 0), k.Tq);
+    const int to = min(max(__ldg(k.cu_q + min(lane + 1, k.B)), from), k.Tq);
+    const unsigned m = __ballot_sync(0xffffffffu, lane < k.B && slot_base(from, lane) <= slot);
+    b = 31 - __clz(m);
+    s.sq = __shfl_sync(0xffffffffu, from, max(b, 0));
+    s.Lq = __shfl_sync(0xffffffffu, to, max(b, 0)) - s.sq;
+  } else {
+    b = sequence_of_slot(k, slot);
+    if (b >= 0) {
+      const Seq x = seq_at(k, b);
+      s.sq = x.sq;
+      s.Lq = x.Lq;
+    }
+  }
+  if (b >= 0 && slot - slot_base(s.sq, b) < tiles(s.Lq)) s.tile = slot - slot_base(s.sq, b);
+  return s;
+}
+
 // Work items.  A sequence's items are `tiles` x `heads` (tiles of queries or of
 // pairs of them, or of keys; heads, pairs of them, or key heads): heads in
 // groups of `group`, so that what a group's items share stays in L2, and within
