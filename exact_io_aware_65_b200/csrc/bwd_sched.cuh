@@ -10,6 +10,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "fa.h"
 #include "pack.cuh"
 #include "sm100.cuh"
@@ -39,13 +41,21 @@ struct Params {
   __nv_bfloat16* dV;
   uint64_t timeout_ns;
   uint32_t* status;
-  // PACKED: the sequences; parts that a key head's query heads are divided
-  // into (each part is an item of its own), and where dK and dV of a part go.
+};
+
+// What a packed launch has besides (a type of its own, as the forward's): the
+// sequences; parts that a key head's query heads are divided into (each part is
+// an item of its own), and where dK and dV of a part go.
+struct PackedParams : Params {
   Pack pk;
   int d, parts;
   float* part;  // [parts][2 (dV, dK)][Tk][Hkv][d], or nullptr: one part, straight to dK and dV
   long long dk_row, dk_head, dv_row, dv_head;  // strides of dK and dV, elements
 };
+template <int MODE>
+using ParamsOf = std::conditional_t<(MODE >= PACKED), PackedParams, Params>;
+// The packed launch's parameters, for branches that only PACKED takes.
+__host__ __device__ __forceinline__ const PackedParams& packed(const Params& p) { return static_cast<const PackedParams&>(p); }
 
 // Heads per scheduling group.  The group's Q and dO tiles (bf16) and fp32
 // dQ accumulator rows are the backward's working set in L2, kept to about
@@ -160,7 +170,7 @@ __host__ __device__ __forceinline__ Step next_step(const Params& p, const Item& 
 
 // Packed sequences: a sequence's items are its key tiles (the first see the
 // most query tiles under a causal mask) times the parts of its key heads.
-__host__ __device__ __forceinline__ pack::Units packed_units(const Params& p, const pack::Seq& s) {
+__host__ __device__ __forceinline__ pack::Units packed_units(const PackedParams& p, const pack::Seq& s) {
   pack::Units u;
   u.tiles = pack::tiles(s.Lk);
   u.heads = p.pk.Hkv * p.parts;
@@ -171,7 +181,7 @@ __host__ __device__ __forceinline__ pack::Units packed_units(const Params& p, co
   return u;
 }
 
-__host__ __device__ __forceinline__ Item packed_item(const Params& p, const pack::Seq& s, int b, const pack::Place& at) {
+__host__ __device__ __forceinline__ Item packed_item(const PackedParams& p, const pack::Seq& s, int b, const pack::Place& at) {
   Item it;
   it.bh = 0;
   it.j = at.tile;

@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     main_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                 const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapdO,
                 const __grid_constant__ CUtensorMap mapdK, const __grid_constant__ CUtensorMap mapdV,
-                const Params p) {
+                const ParamsOf<MODE> p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
 
@@ -511,8 +511,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       it.hk = a.y;
       it.part = a.z;
       it.slot = a.w;
-      it.g0 = it.part * p.pk.G / p.parts;
-      it.g1 = (it.part + 1) * p.pk.G / p.parts;
+      it.g0 = it.part * packed(p).pk.G / packed(p).parts;
+      it.g1 = (it.part + 1) * packed(p).pk.G / packed(p).parts;
       it.sq = b.x;
       it.Lq = b.y;
       it.sk = b.z;
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   };
   // First row of a step's query tile in the workspace's padded rows, and their number.
   auto row_of = [&](const Item& it, const Step& q) -> size_t {
-    if (MODE == PACKED) return ((size_t)(it.slot + q.i) * p.pk.Hq + it.hk * p.pk.G + q.g) * BQ;
+    if (MODE == PACKED) return ((size_t)(it.slot + q.i) * packed(p).pk.Hq + it.hk * packed(p).pk.G + q.g) * BQ;
     return (size_t)it.bh * p.Npad + (size_t)q.i * BQ;
   };
   [[maybe_unused]] const size_t ws_rows = (size_t)p.BH * p.Npad;  // PACKED: BH heads, Npad rows of all slots
@@ -574,27 +574,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         if (idx > p.n_items) idx = p.n_items;
         Item it;
-        if (MODE == PACKED) {
+        if (MODE != PACKED) {  // every role looks the item up (published first: 2% faster at d = 64)
+          item_ring[slot] = idx;
+          mbar_arrive(&item_full[slot]);
+          if (idx >= p.n_items) break;
+          it = item_at<MODE>(p, idx);
+        } else {
           int b;
           pack::Seq sq;
           pack::Place at;
-          if (idx < p.n_items && pack::locate(p.pk, walk, idx, p.n_items, [&](const pack::Seq& x) { return packed_units(p, x); },
+          if (idx < p.n_items && pack::locate(packed(p).pk, walk, idx, p.n_items, [&](const pack::Seq& x) { return packed_units(packed(p), x); },
                                               [](const pack::Seq& x) { return x.Lq; }, b, sq, at))
-            it = packed_item(p, sq, b, at);
+            it = packed_item(packed(p), sq, b, at);
           else
             idx = p.n_items;
-        } else if (idx < p.n_items) {
-          it = item_at<MODE>(p, idx);
-        }
-        if (lead) {
-          item_ring[slot] = idx;
-          if (MODE == PACKED && idx < p.n_items) {
-            item_desc[slot][0] = make_int4(it.j, it.hk, it.part, it.slot);
-            item_desc[slot][1] = make_int4(it.sq, it.Lq, it.sk, it.Lk);
+          if (lead) {
+            item_ring[slot] = idx;
+            if (idx < p.n_items) {
+              item_desc[slot][0] = make_int4(it.j, it.hk, it.part, it.slot);
+              item_desc[slot][1] = make_int4(it.sq, it.Lq, it.sk, it.Lk);
+            }
+            mbar_arrive(&item_full[slot]);
           }
-          mbar_arrive(&item_full[slot]);
+          if (idx >= p.n_items) break;
         }
-        if (idx >= p.n_items) break;
         if (lead) ok = mbar_wait(&kv_empty, (item_iter & 1) ^ 1, w);
         if (lead && ok) {
           const int yq = MODE == PACKED ? -pack::pad(it.Lq) : 0, yk = MODE == PACKED ? -pack::pad(it.Lk) : 0;
@@ -611,7 +614,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint8_t* q = sQD + st * 2 * C::TILE_BYTES;
             const size_t row0 = row_of(it, i);
             uint8_t* ld = smem + C::OFF_LD + st * 1024;
-            const int head = MODE == PACKED ? it.hk * p.pk.G + i.g : it.bh;
+            const int head = MODE == PACKED ? it.hk * packed(p).pk.G + i.g : it.bh;
             ok = mbar_wait(&q_empty[st], par, w);
             if (!ok) break;
             mbar_arrive_expect_tx(&q_full[st], C::TILE_BYTES + 512);
@@ -932,20 +935,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const size_t gbase = ((size_t)it.bh * p.Nk + key) * D;
       // PACKED: rows leave one by one, in fp32, where their head has parts, and
       // from a box that begins before the sequence
-      const bool parts = MODE == PACKED && p.part != nullptr;
+      const bool parts = MODE == PACKED && packed(p).part != nullptr;
       const bool by_row = MODE == PACKED && (parts || prow - lane < 0);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {  // 0: dV, 1: dK
         const float mul = g == 0 ? 1.0f : p.scale;
         __nv_bfloat16* dst = (g == 0 ? p.dV : p.dK);
         if (MODE == PACKED)
-          dst += (long long)(it.sk + prow) * (g == 0 ? p.dv_row : p.dk_row) + it.hk * (g == 0 ? p.dv_head : p.dk_head);
+          dst += (long long)(it.sk + prow) * (g == 0 ? packed(p).dv_row : packed(p).dk_row) + it.hk * (g == 0 ? packed(p).dv_head : packed(p).dk_head);
         else
           dst += gbase;
         // fp32 row of this item's part
-        float* fdst = MODE == PACKED ? p.part + ((((long long)it.part * 2 + g) * p.pk.Tk + it.sk + prow) * p.pk.Hkv + it.hk) * D
+        float* fdst = MODE == PACKED ? packed(p).part + ((((long long)it.part * 2 + g) * packed(p).pk.Tk + it.sk + prow) * packed(p).pk.Hkv + it.hk) * D
                                      : nullptr;
-        const bool row_ok = MODE != PACKED || !store || FA_IN_BOUNDS(p.status, it.sk + prow, 1, p.pk.Tk);
+        const bool row_ok = MODE != PACKED || !store || FA_IN_BOUNDS(p.status, it.sk + prow, 1, packed(p).pk.Tk);
         const int colbase = (g == 0 ? C::COL_DV : C::COL_DK) + hf * (D / 2);
         if constexpr (C::EPI_BYTES > 0) {
           // Lane i puts its 64 bytes (four 16-byte chunks, chunk c at slot
@@ -1353,7 +1356,7 @@ static fa_status launch_bwd_packed_d(const PackedProblem& pr, const CUtensorMap&
   const unsigned blocks = (unsigned)(pack::slots(k.Tq, k.B) * k.Hq);
   if (!launch(bwd::packed_prep_kernel<D>, blocks, 256, 0, s, a)) return FA_ERR_CUDA;
   if (k.Tk > 0) {
-    bwd::Params p = {};
+    bwd::PackedParams p = {};
     p.pk = k;
     p.d = D;
     p.BH = k.Hq;

@@ -130,7 +130,7 @@ template <int D, int MODE, int PIPES>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapO,
-               const Params p) {
+               const ParamsOf<MODE> p) {
   using C = Cfg<D, PIPES>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -217,16 +217,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       it.off = it.nkb - pack::tiles(it.Lq);
       if (MODE == SPLIT) {
         it.part = a.x >> 24;
-        take_part(p, it);
+        take_part(packed(p), it);
       }
     }
   };
+  // (Without packed sequences the MMA warps look the item up themselves, after their
+  // check of idx: 1% faster at d = 128 than in here.)
   auto take_item = [&](int q, uint32_t k, int& idx, Item& it) -> bool {
     const uint32_t slot = k % RING;
     if (!mbar_wait(&item_full[q][slot], (k / RING) & 1, w)) return false;
     read_item(q, slot, idx, it);
     mbar_arrive(&item_empty[q][slot]);
-    if (MODE < PACKED && idx < p.n_items) it = item_at<MODE>(p, idx);
     return true;
   };
   auto give_back = [&](int q, uint32_t k) {
@@ -288,11 +289,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             int b;
             pack::Seq sq;
             pack::Place at;
-            if (idx < p.n_items && pack::locate(p.pk, walk, idx, p.n_items, [&](const pack::Seq& x) { return packed_units(p, x); },
+            if (idx < p.n_items && pack::locate(packed(p).pk, walk, idx, p.n_items, [&](const pack::Seq& x) { return packed_units(packed(p), x); },
                                                 [](const pack::Seq& x) { return x.Lk; }, b, sq, at)) {
-              it = packed_item(p, sq, at);
+              it = packed_item(packed(p), sq, at);
               if (MODE == SPLIT) {
-                take_part(p, it);
+                take_part(packed(p), it);
                 if (it.part >= it.parts) continue;  // the item has fewer parts: nothing to do
               }
             } else {
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ok = await(&q_empty[q], (item_iter & 1) ^ 1);
         if (!ok) break;
         const int yq = MODE >= PACKED ? -pack::pad(it.Lq) : 0, yk = MODE >= PACKED ? -pack::pad(it.Lk) : 0;
-        const int hk = MODE >= PACKED ? it.h0 / p.pk.G : it.bh;
+        const int hk = MODE >= PACKED ? it.h0 / packed(p).pk.G : it.bh;
         if (lead) {
           mbar_arrive_expect_tx(&q_full[q], C::TILE_BYTES * (it.has1 ? 2 : 1));
           load(sQ + q * C::TILE_BYTES, &mapQ, &q_full[q], yq + it.q0 * BM, it.sq, MODE >= PACKED ? it.h0 : it.bh);
@@ -421,6 +422,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           Item it;
           ok = take_item(q, item_iter, idx, it);
           if (!ok || idx >= p.n_items) break;
+          if constexpr (MODE < PACKED) it = item_at<MODE>(p, idx);
           const bool mine = C::DUAL || t == 0 || it.has1;
           const int qt = (C::DUAL || t == 0) ? it.q0 : it.q1;
           ok = mbar_wait(&q_full[q], item_iter & 1, w);
@@ -477,6 +479,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         Item it;
         ok = take_item(0, item_iter, idx, it);
         if (!ok || idx >= p.n_items) break;
+        if constexpr (MODE < PACKED) it = item_at<MODE>(p, idx);
         const int tiles = it.has1 ? 2 : 1;  // tiles [0, tiles) exist
         ok = mbar_wait(&q_full[0], item_iter & 1, w);
         if (!ok) break;
@@ -762,17 +765,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool partial = false;
       if constexpr (MODE == SPLIT) {
         partial = it.parts > 1;
-        if (partial && prow >= 0 && FA_IN_BOUNDS(p.status, it.sq + prow, 1, p.pk.Tq)) {
-          p.part_ml[((size_t)it.part * p.pk.Hq + head) * p.pk.Tq + it.sq + prow] = make_float2(m, l);
+        if (partial && prow >= 0 && FA_IN_BOUNDS(p.status, it.sq + prow, 1, packed(p).pk.Tq)) {
+          packed(p).part_ml[((size_t)it.part * packed(p).pk.Hq + head) * packed(p).pk.Tq + it.sq + prow] = make_float2(m, l);
         }
         if (partial) {
-          float4* row_o = reinterpret_cast<float4*>(p.part_o + (((long long)it.part * p.pk.Hq + head) * p.pk.Tq + it.sq + prow) * D);
+          float4* row_o = reinterpret_cast<float4*>(packed(p).part_o + (((long long)it.part * packed(p).pk.Hq + head) * packed(p).pk.Tq + it.sq + prow) * D);
 #pragma unroll
           for (int c = 0; c < D; c += 32) {
             uint32_t v[32];
             FA_TMEM_LD_X32(t_o + c, v);
             tc_wait_ld();
-            if (prow >= 0 && FA_IN_BOUNDS(p.status, it.sq + prow, 1, p.pk.Tq)) {
+            if (prow >= 0 && FA_IN_BOUNDS(p.status, it.sq + prow, 1, packed(p).pk.Tq)) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 row_o[c / 4 + i] = live ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
@@ -809,8 +812,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               pk[i] = live ? pack_bf16x2(o.x, o.y) : 0u;
             }
             if (by_row) {
-              const long long at = (long long)(it.sq + prow) * p.o_row + head * p.o_head + 64 * g + c;
-              if (prow >= 0 && FA_IN_BOUNDS(p.status, it.sq + prow, 1, p.pk.Tq)) {
+              const long long at = (long long)(it.sq + prow) * packed(p).o_row + head * packed(p).o_head + 64 * g + c;
+              if (prow >= 0 && FA_IN_BOUNDS(p.status, it.sq + prow, 1, packed(p).pk.Tq)) {
                 uint4* o = reinterpret_cast<uint4*>(p.O + at);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
@@ -835,8 +838,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (partial) {
         // the join writes O and LSE
       } else if (MODE >= PACKED) {
-        const size_t at = (size_t)head * p.pk.Tq + it.sq + prow;
-        if (prow >= 0 && FA_IN_BOUNDS(p.status, at, 1, (size_t)p.pk.Hq * p.pk.Tq))
+        const size_t at = (size_t)head * packed(p).pk.Tq + it.sq + prow;
+        if (prow >= 0 && FA_IN_BOUNDS(p.status, at, 1, (size_t)packed(p).pk.Hq * packed(p).pk.Tq))
           p.LSE[at] = live ? (m + log2f(l)) * LN2 : -INFINITY;
       } else if (row < p.N && FA_IN_BOUNDS(p.status, (size_t)it.bh * p.N + row, 1, (size_t)p.BH * p.N))
         p.LSE[(size_t)it.bh * p.N + row] = live ? (m + log2f(l)) * LN2 : -INFINITY;
@@ -860,7 +863,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 constexpr int MAX_PARTS = 32;  // a lane holds a part's maximum and sum
 constexpr int JOIN_ROWS = 16, JOIN_BLOCKS = BM / JOIN_ROWS;
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const Params p) {
+__global__ void __launch_bounds__(256) join_kernel(const PackedParams p) {
   const int tile = blockIdx.x / JOIN_BLOCKS;
   const int slot = tile / p.pk.Hq, h = tile % p.pk.Hq;
   const int b = pack::sequence_of_slot(p.pk, slot);
@@ -1012,7 +1015,7 @@ fa_status launch_fwd_packed(const PackedProblem& pr, const Rows& Q, const Rows& 
       !make_map_packed(&mV, keys ? V : Q, keys ? k.Tk : k.Tq, keys ? k.Hkv : k.Hq, pr.d) ||
       !make_map_rows(&mO, O, k.Tq, k.Hq, pr.d, 64, 32))
     return FA_ERR_CUDA;
-  fwd::Params p = {};
+  fwd::PackedParams p = {};
   p.pk = k;
   p.d = pr.d;
   const bool dual = pr.d == 64;

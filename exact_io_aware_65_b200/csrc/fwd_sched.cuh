@@ -8,6 +8,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "fa.h"
 #include "pack.cuh"
 #include "sm100.cuh"
@@ -37,16 +39,26 @@ struct Params {
   uint64_t timeout_ns;
   uint32_t* status;
   uint32_t slot;  // scheduler counter slot of this launch
-  Pack pk;        // packed sequences (PACKED)
-  int by_heads;   // PACKED: an item's two tiles are two heads' of one query tile
+};
+
+// What the packed launches have besides.  (Of its own type: with these fields in
+// Params, nvcc spilled other registers of the fixed-size kernels, which took 3%
+// longer at d = 128 for it.)
+struct PackedParams : Params {
+  Pack pk;
+  int by_heads;  // an item's two tiles are two heads' of one query tile
   int d;
-  long long o_row, o_head;  // PACKED: strides of O, elements
+  long long o_row, o_head;  // strides of O, elements
   // SPLIT: parts of an item's key tiles, at most; each leaves its unnormalised O
   // [parts][Hq][Tq][d] and (m, l) [parts][Hq][Tq].
   int parts;
   float* part_o;
   float2* part_ml;
 };
+template <int MODE>
+using ParamsOf = std::conditional_t<(MODE >= PACKED), PackedParams, Params>;
+// The packed launch's parameters, for branches that only MODE >= PACKED takes.
+__host__ __device__ __forceinline__ const PackedParams& packed(const Params& p) { return static_cast<const PackedParams&>(p); }
 
 // Heads per scheduling group.  The group's K and V tiles are the forward's
 // working set in L2, kept to about 32 MiB; above that, more heads per group
@@ -109,13 +121,13 @@ __host__ __device__ __forceinline__ int packed_end(const Params& p, int nkb, int
 
 // SPLIT: the parts that `tiles` key tiles are divided into: at least eight tiles
 // each, since a part costs about two tiles' time before and after them.
-__host__ __device__ __forceinline__ int parts_of(const Params& p, int tiles) { return max(1, min(p.parts, tiles / 8)); }
+__host__ __device__ __forceinline__ int parts_of(const PackedParams& p, int tiles) { return max(1, min(p.parts, tiles / 8)); }
 // The later query tile of the item that query tile qt of nq belongs to.
-__host__ __device__ __forceinline__ int last_tile(const Params& p, int nq, int qt) {
+__host__ __device__ __forceinline__ int last_tile(const PackedParams& p, int nq, int qt) {
   return p.tiles_per_item == 2 && !p.by_heads ? nq - 1 - (nq - 1 - qt) / 2 * 2 : qt;
 }
 // The part's key tiles (none for a part past the item's parts).
-__host__ __device__ __forceinline__ void take_part(const Params& p, Item& it) {
+__host__ __device__ __forceinline__ void take_part(const PackedParams& p, Item& it) {
   const int e = packed_end(p, it.nkb, it.off, it.has1 ? it.q1 : it.q0);
   it.parts = parts_of(p, e);
   it.j0 = it.part < it.parts ? e * it.part / it.parts : 0;
@@ -126,7 +138,7 @@ __host__ __device__ __forceinline__ void take_part(const Params& p, Item& it) {
 // d = 128 one query tile of two heads that share their keys where the heads of
 // a key head come in pairs (both see the same keys, and a sequence of one tile
 // still fills the item), else two neighbouring tiles, from the end.
-__host__ __device__ __forceinline__ pack::Units packed_units(const Params& p, const pack::Seq& s) {
+__host__ __device__ __forceinline__ pack::Units packed_units(const PackedParams& p, const pack::Seq& s) {
   pack::Units u;
   const int nq = pack::tiles(s.Lq), per = p.by_heads ? 2 : 1;
   u.tiles = p.tiles_per_item == 2 && !p.by_heads ? (nq + 1) / 2 : nq;
@@ -138,7 +150,7 @@ __host__ __device__ __forceinline__ pack::Units packed_units(const Params& p, co
   return u;
 }
 
-__host__ __device__ __forceinline__ Item packed_item(const Params& p, const pack::Seq& s, const pack::Place& place) {
+__host__ __device__ __forceinline__ Item packed_item(const PackedParams& p, const pack::Seq& s, const pack::Place& place) {
   Item it;
   const pack::Place at{place.tile, place.head / p.parts};
   it.part = place.head % p.parts;

@@ -39,14 +39,14 @@ bool shown(int causal, int i_tile, int j_tile, int off, int r, int c, int Lk) {
 
 void check(const Pack& k, int d, int kind, int parts) {
   namespace P = fa::pack;
-  fa::fwd::Params f = {};
+  fa::fwd::PackedParams f = {};
   f.pk = k;
   f.d = d;
   f.mask_kind = kind;
   f.tiles_per_item = d == 64 ? 1 : 2;
   f.by_heads = d == 128 && k.G % 2 == 0;
   f.parts = 1;
-  fa::bwd::Params w = {};
+  fa::bwd::PackedParams w = {};
   w.pk = k;
   w.d = d;
   w.mask_kind = kind;
@@ -96,7 +96,7 @@ void check(const Pack& k, int d, int kind, int parts) {
       if (x != 1) fail("tile missed", b, x, 0, 0);
     // ---- forward with divided keys: an item's parts cover its key tiles once,
     // and the join counts the parts that the items have
-    fa::fwd::Params g = f;
+    fa::fwd::PackedParams g = f;
     g.parts = 1 + rnd(6);
     std::vector<int> visits((size_t)k.Hq * nq * std::max(nk, 1), 0), parts_seen((size_t)k.Hq * nq, 0);
     const P::Units ug = fa::fwd::packed_units(g, s);
