@@ -250,8 +250,9 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, in
 }
 
 // The sum of what the warps before this one put into v[32].
-__device__ __forceinline__ int sum_before(const int* v, int warp, int lane) {
-  int x = lane < warp ? v[lane] : 0;
+template <typename T>
+__device__ __forceinline__ T sum_before(const T* v, int warp, int lane) {
+  T x = lane < warp ? v[lane] : T(0);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
@@ -260,7 +261,8 @@ __device__ __forceinline__ int sum_before(const int* v, int warp, int lane) {
 // The positions that stay; the CTA's (sequence, head) in p.kept, and how many.
 __device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys) {
   __shared__ uint32_t hist[SEL_BINS];
-  __shared__ int above_w[32], tie_w[32];
+  __shared__ int above_w[32];
+  __shared__ uint32_t both_w[32];
   __shared__ uint32_t sh_digit;
   __shared__ int sh_need, sh_count;
   const int bh = blockIdx.x, b = bh / p.Hkv, h = bh % p.Hkv;
@@ -279,7 +281,26 @@ __device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys)
   if (pick == 0) return left;
   const float* w = p.W + b * p.w_batch + h * p.w_head;
   const bool cached = old <= SEL_SMEM_KEYS;
-  auto key_at = [&](int i) { return cached ? keys[i] : order_key(__ldg(w + i)); };
+  // the keys from position i on, four a load where i is a multiple of 4 (any
+  // value past the last one)
+  auto keys_at = [&](int i, auto& k) {
+    constexpr int N = sizeof(k) / 4;
+    if (cached && N == 1) {
+      k[0] = i < old ? keys[i] : 0u;
+    } else if (cached) {
+#pragma unroll
+      for (int u = 0; u < N / 4; ++u) {
+        const uint4 x = i + 4 * u < old ? *reinterpret_cast<const uint4*>(keys + i + 4 * u) : make_uint4(0u, 0u, 0u, 0u);
+        k[4 * u] = x.x;
+        k[4 * u + 1] = x.y;
+        k[4 * u + 2] = x.z;
+        k[4 * u + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < N; ++u) k[u] = i + u < old ? order_key(__ldg(w + i + u)) : 0u;
+    }
+  };
   hist[tid] = hist[tid + SEL_THREADS] = 0u;
   __syncthreads();
   auto count = [&](uint32_t digit, bool in) {
@@ -299,7 +320,7 @@ __device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys)
   int need = pick, shift = 21;
   for (;;) {
     if (shift == 21) {
-      constexpr int U = 4;  // loads in flight
+      constexpr int U = 8;  // loads in flight
       for (int i0 = warp * 32; i0 < old; i0 += SEL_THREADS * U) {
         float v[U];
 #pragma unroll
@@ -310,6 +331,7 @@ __device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int i = i0 + u * SEL_THREADS + lane;
+          if (i - lane >= old) break;
           const uint32_t k = order_key(v[u]);
           if (cached && i < old) keys[i] = k;
           count(k >> 21, i < old);
@@ -317,11 +339,31 @@ __device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys)
       }
     } else {
       const int up = shift == 10 ? 21 : 10;  // bits already known
-      for (int i0 = warp * 32; i0 < old; i0 += SEL_THREADS) {
-        const int i = i0 + lane;
-        const uint32_t k = i < old ? key_at(i) : 0u;
-        count(shift == 10 ? (k >> 10) & 2047u : k & 1023u, i < old && (k >> up) == digits);
-      }
+      auto count_keys = [&](auto per) {
+        constexpr int N = decltype(per)::value;
+        for (int i0 = warp * 32 * N; i0 < old; i0 += SEL_THREADS * N) {
+          const int i = i0 + N * lane;
+          uint32_t k[N];
+          keys_at(i, k);
+          bool in[N], all = true;
+#pragma unroll
+          for (int u = 0; u < N; ++u) {
+            in[u] = i + u < old && (k[u] >> up) == digits;
+            k[u] = shift == 10 ? (k[u] >> 10) & 2047u : k[u] & 1023u;
+            all = all && in[u] && k[u] == k[0];
+          }
+          const uint32_t first = __shfl_sync(0xffffffffu, k[0], 0);
+          if (__all_sync(0xffffffffu, all && k[0] == first)) {
+            if (lane == 0) atomicAdd(&hist[first], 32u * N);
+            continue;
+          }
+#pragma unroll
+          for (int u = 0; u < N; ++u)
+            if (in[u]) atomicAdd(&hist[k[u]], 1u);
+        }
+      };
+      if (old <= SEL_THREADS) count_keys(std::integral_constant<int, 1>());
+      else count_keys(std::integral_constant<int, 4>());
     }
     __syncthreads();
     // thread T has the bins 2047 - 2 T and 2046 - 2 T, so that threads go down
@@ -350,40 +392,61 @@ __device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys)
     if (shift == 0 || need == sh_count) break;
     shift = shift == 21 ? 10 : 0;
   }
-  // Keys above `digits` stay, and the first `need` that share them.  Each warp
-  // takes a stretch of positions, counts, and then places.
-  const int per = ((old + 31) / 32 + 31) / 32 * 32;
-  const int i0 = min(old, warp * per), i1 = min(old, i0 + per);
-  int above = 0, ties = 0;
-  for (int i = i0 + lane; i - lane < i1; i += 32) {
-    const uint32_t k = i < i1 ? key_at(i) >> shift : 0u;
-    above += __popc(__ballot_sync(0xffffffffu, i < i1 && k > digits));
-    ties += __popc(__ballot_sync(0xffffffffu, i < i1 && k == digits));
-  }
-  if (lane == 0) {
-    above_w[warp] = above;
-    tie_w[warp] = ties;
-  }
-  __syncthreads();
-  int tie_at = sum_before(tie_w, warp, lane);                     // ties of the warps before,
-  int at = sum_before(above_w, warp, lane) + min(tie_at, need);  // and what they keep
-  const unsigned before_me = (1u << lane) - 1u;
-  for (int i = i0 + lane; i - lane < i1; i += 32) {
-    const uint32_t k = i < i1 ? key_at(i) >> shift : 0u;
-    const unsigned tie = __ballot_sync(0xffffffffu, i < i1 && k == digits);
-    const bool stays = i < i1 && (k > digits || (k == digits && tie_at + __popc(tie & before_me) < need));
-    const unsigned keep = __ballot_sync(0xffffffffu, stays);
-    if (stays) kept[at + __popc(keep & before_me)] = i;
-    at += __popc(keep);
-    tie_at += __popc(tie);
-  }
+  // Keys above `digits` stay, and the first `need` that share them.  A thread
+  // takes N neighbouring positions at a time, and a sum over the block of both
+  // counts (at most 8192 each, in halves of a word) gives it its place.  N = 8
+  // where there are that many: the SM's four schedulers issue for 32 warps, and
+  // with a position a lane, placed by ballots, this took 6300 of the selection's
+  // 21000 cycles for 7500 keys.
+  auto place = [&](auto per) {
+    constexpr int N = decltype(per)::value;
+    int at0 = 0, tie0 = 0;  // what stays of the positions before these, and their ties
+    for (int i0 = 0; i0 < old; i0 += SEL_THREADS * N) {
+      const int i = i0 + N * tid;
+      uint32_t k[N];
+      keys_at(i, k);
+      uint32_t over = 0, tie = 0;
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const uint32_t x = k[u] >> shift;
+        over |= (uint32_t)(i + u < old && x > digits) << u;
+        tie |= (uint32_t)(i + u < old && x == digits) << u;
+      }
+      const uint32_t mine = (uint32_t)__popc(over) | (uint32_t)__popc(tie) << 16;
+      uint32_t before = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+      }
+      if (i0 > 0) __syncthreads();  // both_w of the last round has been read
+      if (lane == 31) both_w[warp] = before;
+      __syncthreads();
+      before += sum_before(both_w, warp, lane) - mine;
+      int ties = tie0 + (int)(before >> 16);
+      int at = at0 + (int)(before & 0xffffu) + min(ties, need) - min(tie0, need);
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const bool is_tie = (tie >> u) & 1u;
+        if (((over >> u) & 1u) || (is_tie && ties < need)) kept[at++] = i + u;
+        ties += is_tie;
+      }
+      if (i0 + SEL_THREADS * N < old) {
+        const uint32_t all = sum_before(both_w, 32, lane);
+        at0 += (int)(all & 0xffffu) + min(tie0 + (int)(all >> 16), need) - min(tie0, need);
+        tie0 += (int)(all >> 16);
+      }
+    }
+  };
+  if (old <= SEL_THREADS) place(std::integral_constant<int, 1>());
+  else place(std::integral_constant<int, 8>());
   return left;
 }
 
 // ROWB > 0: the CTA moves its rows too.
 template <int ROWB>
 __global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParams p) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   const int left = select_rows(p, keys);
   if constexpr (ROWB > 0) {
     __syncthreads();  // kept
@@ -465,7 +528,7 @@ fa_status launch_paged_evict(const PagedCache& c, const Evict& e, cudaStream_t s
   p.status = st;
   // shared memory for the keys a head can have to choose from, when they fit
   const long long most = (long long)c.max_pages * c.page_size - e.recent;
-  const int smem = 4 * (int)(most < 0 ? 0 : most < paged::SEL_SMEM_KEYS ? most : paged::SEL_SMEM_KEYS);
+  const int smem = 4 * (int)(most < 0 ? 0 : most < paged::SEL_SMEM_KEYS ? (most + 3) / 4 * 4 : paged::SEL_SMEM_KEYS);
   // A CTA moves the rows it has selected where that is little (sequences
   // of 500 and 1000 rows cut to 250: 10.3 against 13.3 us), or where there
   // is a CTA for every SM; else a second kernel moves them with all SMs (eight
