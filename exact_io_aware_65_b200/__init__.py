@@ -638,7 +638,9 @@ def paged_evict(weights, k_cache, v_cache, page_table, lens, table_out, budget, 
     ``table_out`` (int32 [B, pages], pages of the same pools that no sequence
     of the call reads).  Returns kept [B, Hkv, budget] int32 (the positions
     kept, then -1) and lens_out [B] int32; ``weights_out`` (fp32
-    [B, Hkv, width]) gets the kept rows' weights, then zeros."""
+    [B, Hkv, width]) gets the kept rows' weights, then zeros.  Nothing is
+    written in place: ``weights_out`` is not ``weights``, ``lens_out`` not
+    ``lens``, and ``table_out`` not ``page_table``."""
     if _fast is not None and stream is None:
         made = _fast.paged_evict(weights, k_cache, v_cache, page_table, lens, table_out, weights_out, kept, lens_out, budget, recent)
         if _taken(made, "fa_paged_evict"):

@@ -492,6 +492,9 @@ fa_status fa_paged_evict(const fa_paged_cache* cache, const int* lens, const int
   if ((long long)max_pages_out * c.page_size < most || wo_len < most) return FA_ERR_INVALID_ARG;
   if (wo_len > (1ll << 30) || budget > (1 << 30) || (long long)c.B * c.Hkv * (budget / 32 + 1) > (1ll << 30))
     return FA_ERR_UNSUPPORTED;
+  // in place, blocks would read what others have written (partly overlapping
+  // buffers are the caller's to avoid)
+  if (lens_out == lens || weights_out == weights || table_out == cache->page_table) return FA_ERR_INVALID_ARG;
   Evict e{lens, table_out, (long long)table_out_stride, max_pages_out, weights, (long long)w_batch_stride,
           (long long)w_head_stride, budget, recent, weights_out, (long long)wo_batch_stride,
           (long long)wo_head_stride, (int)wo_len, kept, lens_out};

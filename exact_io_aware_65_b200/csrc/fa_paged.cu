@@ -9,8 +9,9 @@
 // there.  Bound by the conversion's instructions (8476 tokens of 8 heads of 128
 // into 8 bits: 14.4 us, of which HBM needs 8) or by the chain of dependent loads
 // that finds the row (a step of 64 sequences: 3 us, most of it the launch).
-// Evict.  Bound by the chain of its passes (small caches: 9 us) or by HBM (eight
-// caches of 7000-8192 rows cut to 2048: 14 us to select, 27 to move 137 MB).
+// Evict.  Bound by the chain of its passes (small caches: 8 us) or by HBM (eight
+// caches of 7000-8192 rows cut to 2048, 137 MB read and written: 34 us in a graph,
+// the selection's 11 of them with an eighth of the moves beside it).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math.h>
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // two bits of fraction: weights spread over a few powers of two share no bin
 // with most lanes of a warp, and its additions go to shared memory one by one
 // without waiting for each other (8 bits at a time needed the lanes of equal
-// digit matched first: 38.7 us against 13 for 64 heads of 7000-8192 keys).
+// digit matched first: 38.7 us against 13, then, for 64 heads of 7000-8192 keys).
 constexpr int SEL_THREADS = 1024;
 constexpr int SEL_SMEM_KEYS = 48 * 1024;  // 192 KB
 constexpr int SEL_BINS = 2048;
@@ -189,6 +190,7 @@ struct EvictParams {
   int* lens_out;      // [B]
   int B, Hkv, budget, recent, max_out;
   int chunks;         // blocks of the move kernel for one (sequence, head)
+  int early;          // rows of each that move while others are selected, at most
   Divider page;
   uint32_t* status;
 };
@@ -200,17 +202,23 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// The rows that stay in any case are the last ones; this many of them, kept rows
+// [left - n, left), need no selection before they move.
+__device__ __forceinline__ int early_rows(const EvictParams& p, int len, int left) {
+  return min(p.early, len > p.budget ? p.recent : left);
+}
+
 // Moves kept rows [r0, r0 + step) of head h of sequence b, then their weights:
 // a group of ROWB / 16 lanes per row and pool, MOVE_ROWS rows of K and of V in
-// flight per lane.  Row r goes to position r of the table of destination pages.
+// flight per lane.  Row r, of position pos_of(r), goes to position r of the table
+// of destination pages.
 constexpr int MOVE_ROWS = 4;
 
-template <int ROWB>
-__device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, int left, int r0, int step) {
+template <int ROWB, class Pos>
+__device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, int left, int r0, int step, Pos pos_of) {
   constexpr int LPR = ROWB / 16;
   const int groups = blockDim.x / LPR;
   const int sub = threadIdx.x / LPR, piece = threadIdx.x % LPR;
-  const int* kept = p.kept + ((long long)b * p.Hkv + h) * p.budget;
   const int end = min(left, r0 + step);
   for (int r1 = r0; r1 < end; r1 += groups * MOVE_ROWS) {
     uint4 k[MOVE_ROWS], v[MOVE_ROWS];
@@ -221,7 +229,7 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, in
       dst[i] = -1;
       if (r < end) {
         // (pos < max_pages * page_size; rows past the destination table were refused)
-        const int pos = kept[r], from = p.page(pos), to = p.page(r);
+        const int pos = pos_of(r), from = p.page(pos), to = p.page(r);
         const int page = to < p.max_out ? __ldg(p.table_out + b * p.table_out_stride + to) : -1;
         const long long src =
             row_offset(p.c, __ldg(p.c.table + b * p.c.table_stride + from), pos - from * p.c.page_size);
@@ -246,7 +254,7 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, in
   }
   const float* w = p.W + b * p.w_batch + h * p.w_head;
   float* wo = p.Wout + b * p.wo_batch + h * p.wo_head;
-  for (int r = r0 + threadIdx.x; r < end; r += blockDim.x) wo[r] = __ldg(w + kept[r]);
+  for (int r = r0 + threadIdx.x; r < end; r += blockDim.x) wo[r] = __ldg(w + pos_of(r));
 }
 
 // The sum of what the warps before this one put into v[32].
@@ -443,31 +451,46 @@ __device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys)
   return left;
 }
 
-// ROWB > 0: the CTA moves its rows too.
-template <int ROWB>
+// FUSED: the CTA moves its rows too.  Else the CTAs behind those of the (sequence,
+// head)s, on SMs that had nothing to do, move the rows that need no selection.
+template <int ROWB, bool FUSED>
 __global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParams p) {
   extern __shared__ __align__(16) uint32_t keys[];
+  const int heads = p.B * p.Hkv;
+  if (!FUSED && (int)blockIdx.x >= heads) {
+    constexpr int PER = SEL_THREADS / (ROWB / 16) * MOVE_ROWS;
+    const int chunks = (p.early + PER - 1) / PER;
+    for (int u = (int)blockIdx.x - heads; u < heads * chunks; u += (int)gridDim.x - heads) {
+      const int b = u / chunks / p.Hkv, h = u / chunks % p.Hkv;
+      const int n = clamp_len(p.c, __ldg(p.lens + b)), left = min(n, p.budget);
+      move_rows<ROWB>(p, b, h, left, left - early_rows(p, n, left) + u % chunks * PER, PER,
+                      [&](int r) { return n - left + r; });
+    }
+    return;
+  }
   const int left = select_rows(p, keys);
-  if constexpr (ROWB > 0) {
+  if constexpr (FUSED) {
     __syncthreads();  // kept
     const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
-    move_rows<ROWB>(p, b, h, left, 0, left);
+    const int* kept = p.kept + (long long)blockIdx.x * p.budget;
+    move_rows<ROWB>(p, b, h, left, 0, left, [&](int r) { return kept[r]; });
     float* wo = p.Wout + b * p.wo_batch + h * p.wo_head;
     for (int r = left + threadIdx.x; r < p.wo_len; r += SEL_THREADS) wo[r] = 0.0f;
   }
 }
 
-// The moves alone: p.chunks blocks a (sequence, head).
+// The other rows: p.chunks blocks a (sequence, head).
 constexpr int MOVE_THREADS = 256;
 template <int ROWB>
 __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const EvictParams p) {
   constexpr int PER = MOVE_THREADS / (ROWB / 16) * MOVE_ROWS;
   const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const int b = bh / p.Hkv, h = bh % p.Hkv;
-  const int left = min(clamp_len(p.c, __ldg(p.lens + b)), p.budget);
-  move_rows<ROWB>(p, b, h, left, chunk * PER, PER);
-  // the rest of the weights' row, shared by the blocks, is zero
+  const int n = clamp_len(p.c, __ldg(p.lens + b)), left = min(n, p.budget);
+  const int* kept = p.kept + (long long)bh * p.budget;
+  move_rows<ROWB>(p, b, h, left - early_rows(p, n, left), chunk * PER, PER, [&](int r) { return kept[r]; });
   float* wo = p.Wout + b * p.wo_batch + h * p.wo_head;
+  // the rest of the weights' row, shared by the blocks, is zero
   for (long long r = left + (long long)chunk * MOVE_THREADS + threadIdx.x; r < p.wo_len;
        r += (long long)p.chunks * MOVE_THREADS)
     wo[r] = 0.0f;
@@ -539,14 +562,20 @@ fa_status launch_paged_evict(const PagedCache& c, const Evict& e, cudaStream_t s
   auto run = [&](auto width) -> bool {
     constexpr int W = decltype(width)::value;
     static std::atomic<uint64_t> done[2];
-    auto kern = fused ? paged::select_kernel<W> : paged::select_kernel<0>;
+    auto kern = fused ? paged::select_kernel<W, true> : paged::select_kernel<W, false>;
+    // SMs without a selection move rows meanwhile: 256 KB read and written by
+    // each, which takes about as long (eight caches of 7000-8192 rows: 37.4 us
+    // without them, 34.3 with)
+    const int heads = c.B * c.Hkv, idle = fused ? 0 : num_sms() - heads;
+    const long long fit = idle * (256LL << 10) / ((long long)heads * 4 * W);
+    p.early = (int)(fit < e.recent ? fit : e.recent);
     if (!allow_smem(done[fused], (const void*)kern, 4 * paged::SEL_SMEM_KEYS) ||
-        !launch(kern, (unsigned)(c.B * c.Hkv), paged::SEL_THREADS, smem, s, p))
+        !launch(kern, (unsigned)(heads + (p.early > 0 ? idle : 0)), paged::SEL_THREADS, smem, s, p))
       return false;
     if (fused) return true;
     constexpr int PER = paged::MOVE_THREADS / (W / 16) * paged::MOVE_ROWS;
     p.chunks = (e.budget + PER - 1) / PER;
-    return launch(paged::move_kernel<W>, (unsigned)(c.B * c.Hkv * p.chunks), paged::MOVE_THREADS, 0, s, p);
+    return launch(paged::move_kernel<W>, (unsigned)(heads * p.chunks), paged::MOVE_THREADS, 0, s, p);
   };
   const bool ok = rowb == 64    ? run(std::integral_constant<int, 64>())
                   : rowb == 128 ? run(std::integral_constant<int, 128>())

@@ -323,7 +323,8 @@ fa_status fa_paged_decode(const fa_paged_cache* cache, const fa_rows* Q, int Hq,
  *      -1; lens_out, DEVICE int [B]: min(lens[b], budget); weights_out, DEVICE
  *      fp32 rows of wo_len >= min(budget, max_pages * page_size) entries: the
  *      kept rows' weights, then zeros, ready for the next decode steps.
- * Outputs must not alias inputs. */
+ * Outputs must not alias inputs (FA_ERR_INVALID_ARG where lens_out is lens,
+ * weights_out is weights, or table_out the source's table). */
 fa_status fa_paged_evict(const fa_paged_cache* cache, const int* lens, const int* table_out,
                          int64_t table_out_stride, int max_pages_out, const float* weights,
                          int64_t w_batch_stride, int64_t w_head_stride, int budget, int recent,

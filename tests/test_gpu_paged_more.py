@@ -78,6 +78,39 @@ def test_evict_where_keys_share_their_upper_bits(kind):
             assert kept[b, h].tolist() == ref.evict(w[b, h].tolist(), n - 7 * b, budget, recent)
 
 
+@pytest.mark.parametrize("recent", [0, 50, 600])
+@pytest.mark.parametrize("d,e4m3", [(64, True), (64, False), (128, False)])
+def test_evict_moves_last_rows_while_others_are_selected(d, e4m3, recent):
+    # budgets that a second kernel moves, with SMs to spare: lengths of zero, one,
+    # below, at and just above the budget, and past the rows that move early
+    lens, budget, Hkv, page = [0, 1, 37, 1100, 1101, 1700, 4000], 1100, 3, 24
+    left = [min(n, budget) for n in lens]
+    c = ref.make_cache(lens, Hkv, d, page, e4m3, seed=31, extra_pages=sum(-(-n // page) for n in left) + 2)
+    g = torch.Generator().manual_seed(32)
+    w = torch.rand((len(lens), Hkv, c["table"].shape[1] * page), generator=g)
+    table_out = torch.full((len(lens), -(-budget // page)), -1, dtype=torch.int32)
+    free = list(c["free"])
+    for b, n in enumerate(left):
+        for i in range(-(-n // page)):
+            table_out[b, i] = free.pop()
+    dv = ref.dev(c)
+    wo = torch.full((len(lens), Hkv, budget + 5), 3.0, device="cuda")
+    kept, n_out = fa.paged_evict(w.cuda(), dv["kc"], dv["vc"], dv["table"], dv["lens"], table_out.cuda(), budget, recent, wo)
+    assert fa.device_status() == 0 and n_out.tolist() == left
+    want = [c["kc"].clone(), c["vc"].clone()]
+    for b in range(len(lens)):
+        for h in range(Hkv):
+            k = ref.evict(w[b, h].tolist(), lens[b], budget, recent)
+            assert kept[b, h].tolist() == k + [-1] * (budget - len(k)), (b, h)
+            got = wo[b, h].cpu()
+            assert torch.equal(got[:len(k)], w[b, h, k]) and not got[len(k):].any()
+            at, frm = torch.arange(len(k)), torch.tensor(k, dtype=torch.long)
+            for pool in want:
+                pool[table_out[b, at // page].long(), h, at % page] = pool[c["table"][b, frm // page].long(), h, frm % page]
+    for got, x in ((dv["kc"], want[0]), (dv["vc"], want[1])):
+        assert torch.equal(bits(got.cpu().contiguous()), bits(x.contiguous()))
+
+
 def test_decode_calls_at_once_and_many_after_another():
     # divided units on two streams and in a graph, each with buffers of its own;
     # then more calls than there are rows of counters

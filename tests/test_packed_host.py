@@ -154,3 +154,15 @@ def test_the_binding_refuses_host_tensors_and_other_shapes():
         fa.fwd_packed(x, x, x, cu, cu)
     with pytest.raises(fa.FAError):
         fa.bwd_packed(x, x, x, x, x, torch.zeros(2, 4), cu, cu)
+
+
+def test_evict_refuses_what_it_would_overwrite_while_reading():
+    F = 1 << 20   # an address: nothing is launched
+    c = fa._PagedCache(**dict(K=F, V=F, dtype=0, num_pages=5, page_size=16, Hkv=2, d=64, page_stride=2048, head_stride=1024,
+                              row_stride=64, k_scale=None, v_scale=None, page_table=F, B=3, max_pages=4, table_stride=4))
+    go = lambda lens, out, W, Wo, ln: fa.lib().fa_paged_evict(ctypes.byref(c), lens, out, 2, 2, W, 128, 64, 32, 4, Wo, 64, 32, 32,
+                                                            F + 4096, ln, None)
+    a = [F + 4096 * i for i in range(2, 7)]
+    assert go(a[0], a[1], a[2], a[3], a[0]) == 1      # lens
+    assert go(a[0], a[1], a[2], a[2], a[4]) == 1      # weights
+    assert go(a[0], F, a[2], a[3], a[4]) == 1         # the table
