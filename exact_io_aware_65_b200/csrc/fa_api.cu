@@ -427,12 +427,21 @@ static fa_status check_cache(const fa_paged_cache* c, bool scales, PagedCache* p
   return FA_OK;
 }
 
+// Rows that are written may not lie on top of each other.
+static bool cache_rows_apart(const PagedCache& c) {
+  return (c.num_pages == 1 || c.page_stride > 0) && (c.Hkv == 1 || c.head_stride > 0) && (c.page_size == 1 || c.row_stride > 0);
+}
+static bool weight_rows_apart(const PagedCache& c, int64_t batch, int64_t head) {
+  return (c.B == 1 || batch > 0) && (c.Hkv == 1 || head > 0);
+}
+
 fa_status fa_paged_append(const fa_paged_cache* cache, const fa_rows* K, const fa_rows* V, const int* cu_seqlens,
                           const int* lens, int T, void* stream) {
   PagedCache c;
   const fa_status st = check_cache(cache, true, &c);
   if (st != FA_OK) return st;
   if (T < 0 || !cu_seqlens || !lens || !aligned(cu_seqlens, 4) || !aligned(lens, 4)) return FA_ERR_INVALID_ARG;
+  if (!cache_rows_apart(c)) return FA_ERR_INVALID_ARG;
   if (T > (1 << 30)) return FA_ERR_UNSUPPORTED;
   if (T == 0) return FA_OK;
   if (!valid_rows(K, c.d) || !valid_rows(V, c.d)) return FA_ERR_INVALID_ARG;
@@ -454,10 +463,12 @@ fa_status fa_paged_decode(const fa_paged_cache* cache, const fa_rows* Q, int Hq,
   if (!valid_rows(Q, c.d) || Hq <= 0 || Hq % c.Hkv != 0 || !lens || !aligned(lens, 4)) return FA_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || !isfinite(scale)) return FA_ERR_INVALID_ARG;
   if (!O || !LSE || !aligned(O, 16) || !aligned(LSE, 4)) return FA_ERR_INVALID_ARG;
-  if (weights && (!aligned(weights, 4) || w_batch_stride < 0 || w_head_stride < 0)) return FA_ERR_INVALID_ARG;
+  if (weights && (!aligned(weights, 4) || w_batch_stride < 0 || w_head_stride < 0))
+    return FA_ERR_INVALID_ARG;
   if ((long long)c.B * Hq > (1ll << 24)) return FA_ERR_UNSUPPORTED;
   const size_t need = paged_decode_workspace_bytes(c.B, Hq, c.d, (long long)c.max_pages * c.page_size, weights != nullptr);
   if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return FA_ERR_WORKSPACE;
+  if (weights && !weight_rows_apart(c, w_batch_stride, w_head_stride)) return FA_ERR_INVALID_ARG;
   PagedDecode a;
   a.Q = rows_of(Q);
   a.Hq = Hq;
@@ -487,6 +498,7 @@ fa_status fa_paged_evict(const fa_paged_cache* cache, const int* lens, const int
   if (table_out_stride < 0 || w_batch_stride < 0 || w_head_stride < 0 || wo_batch_stride < 0 || wo_head_stride < 0)
     return FA_ERR_INVALID_ARG;
   if (budget <= 0 || recent < 0 || recent > budget || max_pages_out <= 0) return FA_ERR_INVALID_ARG;
+  if (!cache_rows_apart(c) || !weight_rows_apart(c, wo_batch_stride, wo_head_stride)) return FA_ERR_INVALID_ARG;
   const long long cap = (long long)c.max_pages * c.page_size;
   const long long most = cap < budget ? cap : budget;  // rows a sequence can be left with
   if ((long long)max_pages_out * c.page_size < most || wo_len < most) return FA_ERR_INVALID_ARG;

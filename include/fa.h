@@ -258,7 +258,9 @@ fa_status fa_bwd_packed(const fa_rows* Q, const fa_rows* K, const fa_rows* V, co
  * read only for positions that a sequence has.  A page index outside
  * [0, num_pages) is not followed: its rows count as zeros (append and evict
  * skip them) and the call records FA_ERR_BOUNDS in the device status word.
- * Sequences may share pages that are only read. */
+ * Sequences may share pages that are only read.  Of what a call writes (the
+ * pools of append and evict, weights that come out) no two rows may have the
+ * same address: a stride of 0 is FA_ERR_INVALID_ARG there. */
 typedef enum { FA_CACHE_BF16 = 0, FA_CACHE_E4M3 = 1 } fa_cache_dtype;
 
 typedef struct {

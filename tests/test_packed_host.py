@@ -166,3 +166,19 @@ def test_evict_refuses_what_it_would_overwrite_while_reading():
     assert go(a[0], a[1], a[2], a[3], a[0]) == 1      # lens
     assert go(a[0], a[1], a[2], a[2], a[4]) == 1      # weights
     assert go(a[0], F, a[2], a[3], a[4]) == 1         # the table
+
+
+def test_paged_calls_refuse_outputs_whose_rows_lie_on_top_of_each_other():
+    F = 1 << 20
+    base = dict(K=F, V=F, dtype=0, num_pages=5, page_size=16, Hkv=2, d=64, page_stride=2048, head_stride=1024, row_stride=64,
+                k_scale=None, v_scale=None, page_table=F, B=3, max_pages=4, table_stride=4)
+    r = fa._Rows(data=F, row_stride=128, head_stride=64)
+    lib, ref_of = fa.lib(), ctypes.byref
+    for bad in (dict(page_stride=0), dict(head_stride=0), dict(row_stride=0)):
+        c = fa._PagedCache(**{**base, **bad})
+        assert lib.fa_paged_append(ref_of(c), ref_of(r), ref_of(r), F, F + 64, 5, None) == 1
+        assert lib.fa_paged_evict(ref_of(c), F + 64, F + 128, 2, 2, F, 128, 64, 32, 4, F + 4096, 64, 32, 32, F, F + 256, None) == 1
+    c = fa._PagedCache(**base)
+    for wb, wh in ((0, 64), (128, 0)):
+        assert lib.fa_paged_decode(ref_of(c), ref_of(r), 4, F, 0.1, F, wb, wh, 0, F, F, F, 1 << 40, None) == 1
+        assert lib.fa_paged_evict(ref_of(c), F + 64, F + 128, 2, 2, F, 128, 64, 32, 4, F + 4096, wb, wh, 32, F, F + 256, None) == 1
