@@ -132,6 +132,14 @@ __device__ __forceinline__ uint32_t piece_at(int r, int c) {
   return r * ROWB + ((c ^ (r & 7)) * 16);
 }
 
+// Adds one; releases what the CTA has stored before, and acquires what the others
+// had stored before their additions.
+__device__ __forceinline__ uint32_t count_part(uint32_t* p) {
+  uint32_t r;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(r) : "l"(p) : "memory");
+  return r;
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -648,17 +656,13 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
     }
     if (!whole) {
       // The CTA whose part of the unit comes last joins them all.  (A CTA's barrier
-      // orders its threads' stores before thread 0's fence, and its fence before
+      // orders its threads' stores before thread 0's addition, and that before
       // their loads.)
       const int c0 = owner(total, grid, unit_begin), n = owner(total, grid, unit_begin + w.nblk - 1) - c0 + 1;
       __syncthreads();
       if (tid == 0) {
-        __threadfence();
-        const bool last = atomicAdd(&g_came[p.slot][c0], 1u) == (uint32_t)n - 1;
-        if (last) {
-          g_came[p.slot][c0] = 0u;
-          __threadfence();
-        }
+        const bool last = count_part(&g_came[p.slot][c0]) == (uint32_t)n - 1;
+        if (last) g_came[p.slot][c0] = 0u;
         join_last = last;
       }
       __syncthreads();
