@@ -30,9 +30,9 @@
 // a unit that lies in one CTA is finished there, a part of one goes to the
 // workspace, and the CTA that brings a unit's last part joins its parts, in their
 // order (the same bits each run): a second kernel for that cost 4 us more (one
-// sequence of 777 keys, 32 over 8 heads: 14.4 us against 12.4).
+// sequence of 777 keys, 32 over 8 heads: 14.4 us against 12.4, then; now 10.3).
 // What it comes to: 4 sequences of 30001-32768 keys, 8 key heads of 128, in 8 bits
-// 57 us, 4.5 TB/s (bound by the instructions that widen 8 bits); the same in bf16
+// 55 us, 4.6 TB/s (bound by the instructions that widen 8 bits); the same in bf16
 // 91 us, 5.6 TB/s, near the rate of a plain copy.
 // Kernel 2 (weights), on request: P = 2^(s - LSE log2 e) from the scores that
 // kernel 1 left in the workspace, summed over the group in head order.
