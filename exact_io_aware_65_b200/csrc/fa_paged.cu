@@ -10,7 +10,7 @@
 // into 8 bits: 14.4 us, of which HBM needs 8) or by the chain of dependent loads
 // that finds the row (a step of 64 sequences: 3 us, most of it the launch).
 // Evict.  Bound by the chain of its passes (small caches: 8 us) or by HBM (eight
-// caches of 7000-8192 rows cut to 2048, 137 MB read and written: 34 us in a graph,
+// caches of 7000-8192 rows cut to 2048, 137 MB read and written: 31 us in a graph,
 // the selection's 11 of them with an eighth of the moves beside it).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 constexpr int SEL_THREADS = 1024;
 constexpr int SEL_SMEM_KEYS = 48 * 1024;  // 192 KB
 constexpr int SEL_BINS = 2048;
+constexpr int SEL_ROWS = 4;  // rows of K and V that a lane has on their way, in a CTA of 1024 threads
 
 struct EvictParams {
   Cache c;         // source rows
@@ -209,22 +210,20 @@ __device__ __forceinline__ int early_rows(const EvictParams& p, int len, int lef
 }
 
 // Moves kept rows [r0, r0 + step) of head h of sequence b, then their weights:
-// a group of ROWB / 16 lanes per row and pool, MOVE_ROWS rows of K and of V in
+// a group of ROWB / 16 lanes per row and pool, ROWS rows of K and of V in
 // flight per lane.  Row r, of position pos_of(r), goes to position r of the table
 // of destination pages.
-constexpr int MOVE_ROWS = 4;
-
-template <int ROWB, class Pos>
+template <int ROWB, int ROWS, class Pos>
 __device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, int left, int r0, int step, Pos pos_of) {
   constexpr int LPR = ROWB / 16;
   const int groups = blockDim.x / LPR;
   const int sub = threadIdx.x / LPR, piece = threadIdx.x % LPR;
   const int end = min(left, r0 + step);
-  for (int r1 = r0; r1 < end; r1 += groups * MOVE_ROWS) {
-    uint4 k[MOVE_ROWS], v[MOVE_ROWS];
-    long long dst[MOVE_ROWS];
+  for (int r1 = r0; r1 < end; r1 += groups * ROWS) {
+    uint4 k[ROWS], v[ROWS];
+    long long dst[ROWS];
 #pragma unroll
-    for (int i = 0; i < MOVE_ROWS; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       const int r = r1 + i * groups + sub;
       dst[i] = -1;
       if (r < end) {
@@ -245,7 +244,7 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, in
       }
     }
 #pragma unroll
-    for (int i = 0; i < MOVE_ROWS; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       if (dst[i] < 0) continue;
       const long long at = dst[i] + h * p.c.head_stride + piece * 16;
       *reinterpret_cast<uint4*>(p.c.K + at) = k[i];
@@ -458,12 +457,12 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParam
   extern __shared__ __align__(16) uint32_t keys[];
   const int heads = p.B * p.Hkv;
   if (!FUSED && (int)blockIdx.x >= heads) {
-    constexpr int PER = SEL_THREADS / (ROWB / 16) * MOVE_ROWS;
+    constexpr int PER = SEL_THREADS / (ROWB / 16) * SEL_ROWS;
     const int chunks = (p.early + PER - 1) / PER;
     for (int u = (int)blockIdx.x - heads; u < heads * chunks; u += (int)gridDim.x - heads) {
       const int b = u / chunks / p.Hkv, h = u / chunks % p.Hkv;
       const int n = clamp_len(p.c, __ldg(p.lens + b)), left = min(n, p.budget);
-      move_rows<ROWB>(p, b, h, left, left - early_rows(p, n, left) + u % chunks * PER, PER,
+      move_rows<ROWB, SEL_ROWS>(p, b, h, left, left - early_rows(p, n, left) + u % chunks * PER, PER,
                       [&](int r) { return n - left + r; });
     }
     return;
@@ -473,22 +472,24 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParam
     __syncthreads();  // kept
     const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
     const int* kept = p.kept + (long long)blockIdx.x * p.budget;
-    move_rows<ROWB>(p, b, h, left, 0, left, [&](int r) { return kept[r]; });
+    move_rows<ROWB, SEL_ROWS>(p, b, h, left, 0, left, [&](int r) { return kept[r]; });
     float* wo = p.Wout + b * p.wo_batch + h * p.wo_head;
     for (int r = left + threadIdx.x; r < p.wo_len; r += SEL_THREADS) wo[r] = 0.0f;
   }
 }
 
-// The other rows: p.chunks blocks a (sequence, head).
-constexpr int MOVE_THREADS = 256;
+// The other rows: p.chunks blocks a (sequence, head).  Eight blocks on an SM with two
+// rows a lane: one block's chain of positions and pages hides behind the others'
+// rows (four rows a lane and four blocks: 34.3 us for the call's 30.9).
+constexpr int MOVE_THREADS = 256, MOVE_ROWS = 2;
 template <int ROWB>
-__global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(MOVE_THREADS, 8) move_kernel(const EvictParams p) {
   constexpr int PER = MOVE_THREADS / (ROWB / 16) * MOVE_ROWS;
   const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const int b = bh / p.Hkv, h = bh % p.Hkv;
   const int n = clamp_len(p.c, __ldg(p.lens + b)), left = min(n, p.budget);
   const int* kept = p.kept + (long long)bh * p.budget;
-  move_rows<ROWB>(p, b, h, left - early_rows(p, n, left), chunk * PER, PER, [&](int r) { return kept[r]; });
+  move_rows<ROWB, MOVE_ROWS>(p, b, h, left - early_rows(p, n, left), chunk * PER, PER, [&](int r) { return kept[r]; });
   float* wo = p.Wout + b * p.wo_batch + h * p.wo_head;
   // the rest of the weights' row, shared by the blocks, is zero
   for (long long r = left + (long long)chunk * MOVE_THREADS + threadIdx.x; r < p.wo_len;
@@ -565,7 +566,7 @@ fa_status launch_paged_evict(const PagedCache& c, const Evict& e, cudaStream_t s
     auto kern = fused ? paged::select_kernel<W, true> : paged::select_kernel<W, false>;
     // SMs without a selection move rows meanwhile: 256 KB read and written by
     // each, which takes about as long (eight caches of 7000-8192 rows: 37.4 us
-    // without them, 34.3 with)
+    // without them, 34.3 with, then)
     const int heads = c.B * c.Hkv, idle = fused ? 0 : num_sms() - heads;
     const long long fit = idle * (256LL << 10) / ((long long)heads * 4 * W);
     p.early = (int)(fit < e.recent ? fit : e.recent);
