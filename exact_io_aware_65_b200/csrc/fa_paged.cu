@@ -259,10 +259,7 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, in
 // The sum of what the warps before this one put into v[32].
 template <typename T>
 __device__ __forceinline__ T sum_before(const T* v, int warp, int lane) {
-  T x = lane < warp ? v[lane] : T(0);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+  return __reduce_add_sync(0xffffffffu, lane < warp ? v[lane] : T(0));
 }
 
 // The positions that stay; the CTA's (sequence, head) in p.kept, and how many.
