@@ -39,6 +39,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
+#include <sys/random.h>
+#include <time.h>
 
 #include <type_traits>
 
@@ -51,12 +53,8 @@ namespace paged {
 
 constexpr int ROWS = 16;  // query heads of a unit, at most: 8 in a tile, NB tiles
 constexpr int THREADS = WARPS * 32;
-// Counters of the parts that have come, one a CTA that a divided unit begins in;
-// the CTA that joins a unit puts its counter back to zero.  Each launch takes one
-// of JOIN_SLOTS rows of them: half as many launches may be in flight at once.
-constexpr uint32_t JOIN_SLOTS = 2048;
 constexpr int MAX_GRID = 160;
-__device__ uint32_t g_came[JOIN_SLOTS][MAX_GRID];
+static_assert(MAX_GRID < 1 << COUNT_BITS, "a unit's parts are counted in this many bits");
 
 constexpr float SLACK = 8.0f;  // log2 units a score may lie above the reference maximum
 constexpr int MAX_BATCH = 4096;                 // sequences per launch (prefix of their blocks in shared memory)
@@ -76,7 +74,8 @@ struct DecodeParams {
   float sl2;                // scale * log2(e)
   float* part;              // [2 grid][ROWS][D] unnormalised O
   float2* ml;               // [2 grid][ROWS] (m, l)
-  uint32_t slot;            // row of g_came
+  unsigned long long* came; // [grid] counters of the parts of the unit that begins in a CTA (paged.cuh)
+  unsigned long long tag;   // above their counts
   float* scores;            // [B, Hq, pitch] scaled log2 scores, or nullptr
   long long pitch;
   __nv_bfloat16* O;         // [B, Hq, D]
@@ -132,13 +131,21 @@ __device__ __forceinline__ uint32_t piece_at(int r, int c) {
   return r * ROWB + ((c ^ (r & 7)) * 16);
 }
 
-// Adds one; releases what the CTA has stored before, and acquires what the others
-// had stored before their additions.
-__device__ __forceinline__ uint32_t count_part(uint32_t* p) {
-  uint32_t r;
-  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(r) : "l"(p) : "memory");
-  return r;
-}
+// A counter of parts: each operation releases what the CTA has stored before, and
+// acquires what the others had stored before theirs.
+struct Counter {
+  unsigned long long* p;
+  __device__ __forceinline__ unsigned long long add(unsigned long long n) {
+    unsigned long long r;
+    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], %2;" : "=l"(r) : "l"(p), "l"(n) : "memory");
+    return r;
+  }
+  __device__ __forceinline__ unsigned long long cas(unsigned long long expected, unsigned long long desired) {
+    unsigned long long r;
+    asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;" : "=l"(r) : "l"(p), "l"(expected), "l"(desired) : "memory");
+    return r;
+  }
+};
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
@@ -672,8 +679,9 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
       const int c0 = owner(total, grid, unit_begin), n = owner(total, grid, unit_begin + w.nblk - 1) - c0 + 1;
       __syncthreads();
       if (tid == 0) {
-        const bool last = count_part(&g_came[p.slot][c0]) == (uint32_t)n - 1;
-        if (last) g_came[p.slot][c0] = 0u;
+        Counter came{p.came + c0};
+        const bool last = count_part(came, p.tag) == n - 1;
+        if (last) p.came[c0] = p.tag;
         join_last = last;
       }
       __syncthreads();
@@ -761,10 +769,18 @@ __global__ void __launch_bounds__(W_THREADS) weights_kernel(const DecodeParams p
   }
 }
 
-// The counters of the next launch on `s`, of whatever type.
-static uint32_t next_slot(cudaStream_t s) {
-  static SlotTurn turn;
-  return turn.take(s, JOIN_SLOTS);
+// The process's tag of the counters.
+static unsigned long long join_tag() {
+  static const unsigned long long tag = [] {
+    unsigned long long x = 0;
+    if (getrandom(&x, sizeof(x), GRND_NONBLOCK) != (ssize_t)sizeof(x)) {
+      timespec now;  // no random source: the time in nanoseconds, above the place of this stack
+      clock_gettime(CLOCK_REALTIME, &now);
+      x = ((unsigned long long)now.tv_sec * 1000000000ull + (unsigned long long)now.tv_nsec) << 24 ^ reinterpret_cast<uintptr_t>(&x);
+    }
+    return x >> COUNT_BITS << COUNT_BITS;
+  }();
+  return tag;
 }
 
 // One CTA per SM, at most as many as there are counters.
@@ -773,12 +789,13 @@ static int decode_grid() { return num_sms() < MAX_GRID ? num_sms() : MAX_GRID; }
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct DecodeLayout {
-  size_t part, ml, scores, total;
+  size_t came, part, ml, scores, total;
 };
 static DecodeLayout layout(int B, int Hq, int d, long long cap, bool weights, int grid) {
   DecodeLayout w;
-  w.part = 0;
-  w.ml = align256((size_t)2 * grid * ROWS * d * sizeof(float));
+  w.came = 0;  // first, where every call finds what the last one left
+  w.part = align256((size_t)grid * sizeof(unsigned long long));
+  w.ml = w.part + align256((size_t)2 * grid * ROWS * d * sizeof(float));
   w.scores = w.ml + align256((size_t)2 * grid * ROWS * sizeof(float2));
   w.total = w.scores + (weights ? align256((size_t)B * Hq * ((cap + STEP - 1) / STEP * STEP) * sizeof(float)) : 0);
   return w;
@@ -812,7 +829,6 @@ static fa_status launch_d(paged::DecodeParams p, int B, const PagedDecode& a, in
     p.O = O + (long long)b0 * p.Hq * D;
     p.LSE = LSE + (long long)b0 * p.Hq;
     if (scores) p.scores = scores + (long long)b0 * p.Hq * p.pitch;
-    p.slot = next_slot(s);
     if (!launch(kern, (unsigned)grid, THREADS, smem, s, p)) return FA_ERR_CUDA;
     if (scores) {
       long long chunks = (p.pitch + 4 * W_THREADS - 1) / (4 * W_THREADS);  // four keys a thread
@@ -851,6 +867,8 @@ fa_status launch_paged_decode(const PagedCache& c, const PagedDecode& a, cudaStr
   p.whole = cap <= 4 * paged::BLOCK;
   p.wide = ((c.num_pages - 1) * c.page_stride + (c.page_size - 1) * c.row_stride) * c.elem >= (1ll << 36);
   p.sl2 = a.scale_log2;
+  p.came = reinterpret_cast<unsigned long long*>(ws + w.came);
+  p.tag = paged::join_tag();
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
   p.scores = a.W ? reinterpret_cast<float*>(ws + w.scores) : nullptr;

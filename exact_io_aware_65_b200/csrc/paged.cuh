@@ -98,6 +98,33 @@ __host__ __device__ __forceinline__ int part_slot(int c, long long cta_begin, lo
   return 2 * c + (cta_begin >= unit_begin ? 0 : 1);
 }
 
+// The parts of a unit that is divided between CTAs are counted, and the CTA that
+// brings the last one joins them.  The counter of the unit that begins in CTA c is
+// word c at the head of the call's workspace, which calls that may overlap do not
+// share.  Whatever the workspace holds on entry, a word counts only under the
+// process's tag, 56 random bits above an 8-bit count: a part that meets other
+// contents puts the tag there, and the last one leaves the tag with a count of
+// zero, so that later calls on the same workspace need one addition a part and
+// none has to clear the words first (a launch of its own would cost 2 us of 10).
+// (Other contents pass for the tag with a chance of 2^-56.)
+constexpr int COUNT_BITS = 8;
+// Parts of the unit counted before this one.  Word: add(n) and cas(expected,
+// desired), both atomic, return the word as it was.  A part adds to other contents
+// once at most, so that each of the n parts fails at most n times to replace them.
+#pragma nv_exec_check_disable
+template <class Word>
+__host__ __device__ __forceinline__ int count_part(Word& w, unsigned long long tag) {
+  constexpr unsigned long long COUNT = (1ull << COUNT_BITS) - 1;
+  unsigned long long seen = w.add(1);
+  if (((seen ^ tag) & ~COUNT) == 0) return (int)(seen & COUNT);
+  for (++seen;;) {
+    const unsigned long long was = w.cas(seen, tag | 1u);
+    if (was == seen) return 0;
+    if (((was ^ tag) & ~COUNT) == 0) return (int)(w.add(1) & COUNT);
+    seen = was;
+  }
+}
+
 // What the walk goes by.
 struct Work {
   const Cache* c;

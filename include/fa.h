@@ -295,7 +295,8 @@ fa_status fa_paged_append(const fa_paged_cache* cache, const fa_rows* K, const f
  *      page_size]): every key below lens[b] is visible; scale > 0; workspace
  *      (DEVICE, 256-byte aligned, fa_paged_decode_workspace_size() bytes with
  *      max_len = max_pages * page_size; contents irrelevant on entry; calls
- *      that may overlap need one each).
+ *      that may overlap, replayed ones among them, need one each: all that
+ *      a call leaves on the device besides its outputs lies there).
  * Out: O [B, Hq, d] bf16, LSE [B, Hq] fp32 (natural log), contiguous; a
  *      sequence without keys gets O = 0, LSE = -inf.  weights (may be NULL):
  *      DEVICE fp32 [B, Hkv, max_pages * page_size] with the given strides in
