@@ -60,6 +60,7 @@
 #include "fa_internal.h"
 #include "sm100.cuh"
 #include "fwd_sched.cuh"
+#include "slots.h"
 
 namespace fa {
 namespace fwd {
@@ -68,14 +69,15 @@ constexpr int NUM_THREADS = 384;
 constexpr int RING = 4;              // depth of the item ring the producer fills
 
 // Dynamic schedule.  CTA b starts on item b; after that each CTA claims
-// items gridDim.x, gridDim.x + 1, ... from a counter.  Each launch takes one
-// of SCHED_SLOTS counters (in turn, on the host), and the last CTA to stop
-// claiming puts it back to zero.  Launches that run at the same time (other
-// streams) use other slots, so at most half of SCHED_SLOTS forward launches
-// may be in flight at once (the other half is for captured ones).
-constexpr uint32_t SCHED_SLOTS = 4096;
-__device__ uint32_t g_claim[SCHED_SLOTS];  // dynamic claims so far
-__device__ uint32_t g_done[SCHED_SLOTS];   // CTAs that stopped claiming
+// items gridDim.x, gridDim.x + 1, ... from a counter, and the last CTA to stop
+// claiming puts it back to zero.  A launch outside of graphs takes one of
+// TURN_SLOTS counters, in turn; launches that run at the same time (other
+// streams) use other slots, so at most that many may be in flight at once.  A
+// captured launch runs again and again on the slot that it was captured with: it
+// takes one of GRAPH_SLOTS that no other graph has (next_slot).
+constexpr uint32_t TURN_SLOTS = 4096, GRAPH_SLOTS = 65536;
+__device__ uint32_t g_claim[TURN_SLOTS + GRAPH_SLOTS];  // dynamic claims so far
+__device__ uint32_t g_done[TURN_SLOTS + GRAPH_SLOTS];   // CTAs that stopped claiming
 constexpr float LN2 = 0.69314718055994530942f;
 
 template <int D, int PIPES>
@@ -915,10 +917,29 @@ __global__ void __launch_bounds__(256) join_kernel(const PackedParams p) {
   }
 }
 
-// The counter slot of the next launch on `s`.
-static uint32_t next_slot(cudaStream_t s) {
-  static SlotTurn turn;
-  return turn.take(s, SCHED_SLOTS);
+static OwnedSlots<GRAPH_SLOTS> graph_slots;
+static void CUDART_CB give_back(void* slot) { graph_slots.give((int)reinterpret_cast<intptr_t>(slot)); }
+
+// The counter slot of the next launch on `s`.  A captured launch's slot belongs to
+// its graph, and to all that is made of it, until the last of these is destroyed
+// (and has finished running).  FA_ERR_UNSUPPORTED if every slot has an owner.
+static fa_status next_slot(cudaStream_t s, uint32_t* slot) {
+  static std::atomic<uint32_t> turn{0};
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  cudaGraph_t graph = nullptr;
+  if (cudaStreamGetCaptureInfo(s, &st, nullptr, &graph) != cudaSuccess || st != cudaStreamCaptureStatusActive) {
+    *slot = turn.fetch_add(1u, std::memory_order_relaxed) % TURN_SLOTS;
+    return FA_OK;
+  }
+  const int mine = graph_slots.take();
+  if (mine < 0) return FA_ERR_UNSUPPORTED;
+  *slot = TURN_SLOTS + (uint32_t)mine;
+  cudaUserObject_t owner = nullptr;
+  if (cudaUserObjectCreate(&owner, reinterpret_cast<void*>((intptr_t)mine), give_back, 1, cudaUserObjectNoDestructorSync) !=
+          cudaSuccess ||
+      cudaGraphRetainUserObject(graph, owner, 1, cudaGraphUserObjectMove) != cudaSuccess)
+    (void)cudaGetLastError();  // a graph that cannot own it: the slot is never lent again
+  return FA_OK;
 }
 
 }  // namespace fwd
@@ -954,7 +975,8 @@ fa_status launch_fwd(const Problem& pr, const void* Q, const void* K, const void
   p.LSE = LSE;
   p.timeout_ns = wait_timeout_ns();
   p.status = st;
-  p.slot = fwd::next_slot(s);
+  const fa_status lent = fwd::next_slot(s, &p.slot);
+  if (lent != FA_OK) return lent;
   const int npipe = dual ? 2 : 1;
   const int want = (p.n_items + npipe - 1) / npipe;  // CTAs that get a first item in every pipeline
   const int grid = want < num_sms() ? want : num_sms();
@@ -1037,7 +1059,8 @@ fa_status launch_fwd_packed(const PackedProblem& pr, const Rows& Q, const Rows& 
   p.LSE = LSE;
   p.timeout_ns = wait_timeout_ns();
   p.status = st;
-  p.slot = fwd::next_slot(s);
+  const fa_status lent = fwd::next_slot(s, &p.slot);
+  if (lent != FA_OK) return lent;
   const int npipe = dual ? 2 : 1;
   const int want = (p.n_items + npipe - 1) / npipe;
   const int grid = want < num_sms() ? want : num_sms();

@@ -70,18 +70,6 @@ inline bool launch(void (*kernel)(P...), unsigned grid, int threads, size_t smem
   return cudaGetLastError() == cudaSuccess;
 }
 
-// Counter slots that launches take in turn.  A captured launch keeps its slot
-// for as long as its graph lives, so it takes one from a half of its own: a
-// graph and launches outside it, on another stream, then never meet on a slot.
-struct SlotTurn {
-  std::atomic<uint32_t> next[2];
-  uint32_t take(cudaStream_t s, uint32_t slots) {
-    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    const bool captured = cudaStreamIsCapturing(s, &st) == cudaSuccess && st != cudaStreamCaptureStatusNone;
-    return (captured ? slots / 2 : 0u) + next[captured].fetch_add(1u, std::memory_order_relaxed) % (slots / 2);
-  }
-};
-
 uint64_t wait_timeout_ns();
 // Device address of the calling device's status word (nullptr on failure).
 uint32_t* status_word();

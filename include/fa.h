@@ -37,10 +37,13 @@
  *     the library keeps no allocation between calls.
  *   - Outputs must not alias inputs.
  *   - CUDA graphs: every call can be captured into a graph, after one
- *     eager call on the device has set up the per-device state.  Each
- *     forward launch takes one of 2048 per-device work-counter slots when it
- *     is issued, or, captured, one of 2048 others, which it keeps: one graph
- *     must not be replayed on two streams at once.
+ *     eager call on the device has set up the per-device state.  A forward
+ *     launch uses a work counter on the device: outside of graphs one of
+ *     4096, in turn, so that at most that many may be in flight at once;
+ *     captured, one of 65536 that belongs to its graph until that graph and
+ *     all instances and clones of it are destroyed (FA_ERR_UNSUPPORTED while
+ *     all have an owner).  Different graphs may be replayed at once; two
+ *     instances of one graph, or of its clones, may not.
  *   - Errors: argument problems are reported synchronously, before anything
  *     is launched.  A failed launch returns FA_ERR_CUDA.  Every wait inside
  *     the kernels is bounded in time; a wait that runs out records
@@ -60,7 +63,8 @@ extern "C" {
 typedef enum {
   FA_OK = 0,
   FA_ERR_INVALID_ARG = 1, /* null/misaligned pointer, bad size, bad scale, bad mask kind */
-  FA_ERR_UNSUPPORTED = 2, /* valid request outside this build: d not 64/128, B*H*N or B*H*Nk above 2^37 */
+  FA_ERR_UNSUPPORTED = 2, /* valid request outside this build: d not 64/128, B*H*N or B*H*Nk above 2^37,
+                             no work counter left for a captured launch */
   FA_ERR_CUDA = 3,        /* a CUDA runtime or driver call failed */
   FA_ERR_WORKSPACE = 4,   /* workspace missing or smaller than fa_bwd_workspace_size() */
   FA_ERR_TIMEOUT = 5,     /* a bounded device-side wait ran out (see fa_device_status) */
