@@ -14,6 +14,7 @@
 // the selection's 11 of them with an eighth of the moves beside it).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+#include <limits.h>
 #include <math.h>
 
 #include <type_traits>
@@ -134,9 +135,10 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
   const int held = __ldg(p.lens + b);
   const long long pos = held + (long long)t - __ldg(p.cu + b);
   long long off = -1;
-  if (held >= 0 && pos < (long long)p.c.max_pages * p.c.page_size) {
-    const int i = p.page((int)pos);
-    off = row_offset(p.c, __ldg(p.c.table + b * p.c.table_stride + i), (int)pos - i * p.c.page_size);
+  if (held >= 0) {
+    // (the table spans at most 2^30 positions)
+    const int at = (int)min(pos, (long long)INT_MAX), i = p.page(at);
+    off = row_offset(p.c, page_of(p.c, p.c.table + b * p.c.table_stride, at, i), at - i * p.c.page_size);
   }
   if (off < 0) {
     if (lane == 0) bad_page(p.status);
@@ -204,15 +206,15 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 }
 
 // The rows that stay in any case are the last ones; this many of them, kept rows
-// [left - n, left), need no selection before they move.
-__device__ __forceinline__ int early_rows(const EvictParams& p, int len, int left) {
-  return min(p.early, len > p.budget ? p.recent : left);
-}
+// [left - n, left), need no selection before they move.  (p.early <= recent.)
+__device__ __forceinline__ int early_rows(const EvictParams& p, int left) { return min(p.early, left); }
 
 // Moves kept rows [r0, r0 + step) of head h of sequence b, then their weights:
 // a group of ROWB / 16 lanes per row and pool, ROWS rows of K and of V in
 // flight per lane.  Row r, of position pos_of(r), goes to position r of the table
-// of destination pages.
+// of destination pages.  (0 <= pos_of(r) < max_pages * page_size for r < left: the
+// selection sees to that, whatever happens to lens and weights meanwhile.  A test
+// here instead cost 0.5-1.4 of 30 us.)
 template <int ROWB, int ROWS, class Pos>
 __device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, int left, int r0, int step, Pos pos_of) {
   constexpr int LPR = ROWB / 16;
@@ -227,7 +229,7 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int b, int h, in
       const int r = r1 + i * groups + sub;
       dst[i] = -1;
       if (r < end) {
-        // (pos < max_pages * page_size; rows past the destination table were refused)
+        // (rows past the destination table were refused)
         const int pos = pos_of(r), from = p.page(pos), to = p.page(r);
         const int page = to < p.max_out ? __ldg(p.table_out + b * p.table_out_stride + to) : -1;
         const long long src =
@@ -401,9 +403,12 @@ __device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys)
   // counts (at most 8192 each, in halves of a word) gives it its place.  N = 8
   // where there are that many: the SM's four schedulers issue for 32 warps, and
   // with a position a lane, placed by ballots, this took 6300 of the selection's
-  // 21000 cycles for 7500 keys.
-  auto place = [&](auto per) {
+  // 21000 cycles for 7500 keys.  Keys that do not fit on chip are read again here;
+  // where they are no longer those that were counted, what is placed still stays
+  // within the row, and the row is filled.
+  auto place = [&](auto per, auto again) {
     constexpr int N = decltype(per)::value;
+    constexpr bool AGAIN = decltype(again)::value;
     int at0 = 0, tie0 = 0;  // what stays of the positions before these, and their ties
     for (int i0 = 0; i0 < old; i0 += SEL_THREADS * N) {
       const int i = i0 + N * tid;
@@ -432,18 +437,22 @@ __device__ __forceinline__ int select_rows(const EvictParams& p, uint32_t* keys)
 #pragma unroll
       for (int u = 0; u < N; ++u) {
         const bool is_tie = (tie >> u) & 1u;
-        if (((over >> u) & 1u) || (is_tie && ties < need)) kept[at++] = i + u;
+        if ((((over >> u) & 1u) || (is_tie && ties < need)) && (!AGAIN || at < pick)) kept[at++] = i + u;
         ties += is_tie;
       }
-      if (i0 + SEL_THREADS * N < old) {
+      if (AGAIN || i0 + SEL_THREADS * N < old) {
         const uint32_t all = sum_before(both_w, 32, lane);
         at0 += (int)(all & 0xffffu) + min(tie0 + (int)(all >> 16), need) - min(tie0, need);
         tie0 += (int)(all >> 16);
       }
     }
+    if (AGAIN) {
+      for (int i = at0 + tid; i < pick; i += SEL_THREADS) kept[i] = 0;
+    }
   };
-  if (old <= SEL_THREADS) place(std::integral_constant<int, 1>());
-  else place(std::integral_constant<int, 8>());
+  if (old <= SEL_THREADS) place(std::integral_constant<int, 1>(), std::false_type());
+  else if (cached) place(std::integral_constant<int, 8>(), std::false_type());
+  else place(std::integral_constant<int, 8>(), std::true_type());
   return left;
 }
 
@@ -459,7 +468,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParam
     for (int u = (int)blockIdx.x - heads; u < heads * chunks; u += (int)gridDim.x - heads) {
       const int b = u / chunks / p.Hkv, h = u / chunks % p.Hkv;
       const int n = clamp_len(p.c, __ldg(p.lens + b)), left = min(n, p.budget);
-      move_rows<ROWB, SEL_ROWS>(p, b, h, left, left - early_rows(p, n, left) + u % chunks * PER, PER,
+      move_rows<ROWB, SEL_ROWS>(p, b, h, left, left - early_rows(p, left) + u % chunks * PER, PER,
                       [&](int r) { return n - left + r; });
     }
     return;
@@ -484,9 +493,9 @@ __global__ void __launch_bounds__(MOVE_THREADS, 8) move_kernel(const EvictParams
   constexpr int PER = MOVE_THREADS / (ROWB / 16) * MOVE_ROWS;
   const int bh = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const int b = bh / p.Hkv, h = bh % p.Hkv;
-  const int n = clamp_len(p.c, __ldg(p.lens + b)), left = min(n, p.budget);
+  const int left = p.lens_out[b];  // of the selection, as the positions are
   const int* kept = p.kept + (long long)bh * p.budget;
-  move_rows<ROWB, MOVE_ROWS>(p, b, h, left - early_rows(p, n, left), chunk * PER, PER, [&](int r) { return kept[r]; });
+  move_rows<ROWB, MOVE_ROWS>(p, b, h, left - early_rows(p, left), chunk * PER, PER, [&](int r) { return kept[r]; });
   float* wo = p.Wout + b * p.wo_batch + h * p.wo_head;
   // the rest of the weights' row, shared by the blocks, is zero
   for (long long r = left + (long long)chunk * MOVE_THREADS + threadIdx.x; r < p.wo_len;

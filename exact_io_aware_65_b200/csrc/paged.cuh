@@ -33,11 +33,16 @@ __host__ __device__ __forceinline__ long long row_offset(const Cache& c, int pag
   return page * c.page_stride + slot * c.row_stride;
 }
 
-// The page index of position `pos` of sequence b; -1 past the table's width.
-__host__ __device__ __forceinline__ int page_of(const Cache& c, int b, long long pos) {
-  const long long i = pos / c.page_size;
+// The page index of position `pos`, entry i = pos / page_size of a sequence's row of
+// the table; -1 for a position that the table does not span (i is then not used).
+template <class Int>
+__host__ __device__ __forceinline__ int page_of(const Cache& c, const int* row, Int pos, Int i) {
   if (pos < 0 || i >= c.max_pages) return -1;
-  return ld_ro(c.table + b * c.table_stride + i);
+  return ld_ro(row + i);
+}
+// The same of sequence b, by division.
+__host__ __device__ __forceinline__ int page_of(const Cache& c, int b, long long pos) {
+  return page_of(c, c.table + b * c.table_stride, pos, pos / c.page_size);
 }
 
 // Division of n < 2^31 by a number fixed for the launch: with 2^(s-1) < d <= 2^s
