@@ -755,7 +755,8 @@ __global__ void __launch_bounds__(W_THREADS) weights_kernel(const DecodeParams p
     for (int r = 0; r < p.G; ++r) {
       // (rows are 16-byte aligned, and end on a whole step behind the last key)
       const float4 s = *reinterpret_cast<const float4*>(p.scores + (first + r) * p.pitch + j);
-      const float lse = __ldg(p.LSE + first + r) * LOG2E;
+      // (a head all of whose scores are -inf draws nothing, as its O is zero)
+      const float l = __ldg(p.LSE + first + r), lse = l == -INFINITY ? 0.0f : l * LOG2E;
       sum.x += ex2_approx(s.x - lse);
       sum.y += ex2_approx(s.y - lse);
       sum.z += ex2_approx(s.z - lse);

@@ -302,7 +302,8 @@ fa_status fa_paged_append(const fa_paged_cache* cache, const fa_rows* K, const f
  *      that may overlap, replayed ones among them, need one each: all that
  *      a call leaves on the device besides its outputs lies there).
  * Out: O [B, Hq, d] bf16, LSE [B, Hq] fp32 (natural log), contiguous; a
- *      sequence without keys gets O = 0, LSE = -inf.  weights (may be NULL):
+ *      sequence without keys gets O = 0, LSE = -inf, and so does a head all of
+ *      whose scores are -inf (it gives its keys no weight).  weights (may be NULL):
  *      DEVICE fp32 [B, Hkv, max_pages * page_size] with the given strides in
  *      elements; entry (b, k, j), j < lens[b], is set to (accumulate = 0), or
  *      raised by, the attention that key j of key head k drew, summed over its
