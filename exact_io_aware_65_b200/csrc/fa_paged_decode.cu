@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
       reinterpret_cast<uint4*>(p.O + (long long)b * p.Hq * D)[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = tid; i < p.Hq; i += THREADS) p.LSE[(long long)b * p.Hq + i] = -INFINITY;
   }
-  if (w.at >= w.end) return;
+  if (!at_hand(w)) return;
 
   // ---- the copies run up to NU units ahead of the products (K, V, K, V, ...),
   // the page lookups a step ahead of the copies.  Lane r (and r + 16) looks up
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(THREADS, 1) partial_kernel(const DecodeParams 
   }
 
   uint32_t got = 0;  // ring slot of the next unit to use
-  while (w.at < w.end) {
+  while (at_hand(w)) {
     // ---- a unit, or this CTA's part of it
     const int hk = w.hu / p.HB, row0 = (w.hu % p.HB) * R;
     const int heads = min(R, p.G - row0);  // query heads in use

@@ -91,6 +91,7 @@ __host__ __device__ __forceinline__ long long share(long long total, int grid, i
 // The CTA that holds block x: the largest c with share(c) <= x.
 __host__ __device__ __forceinline__ int owner(long long total, int grid, long long x) {
   int c = (int)quotient(x * grid, total);
+  if (c >= grid) c = grid - 1;  // x past the last block
   while (c + 1 < grid && share(total, grid, c + 1) <= x) ++c;
   while (c > 0 && share(total, grid, c) > x) --c;
   return c;
@@ -130,7 +131,9 @@ __host__ __device__ __forceinline__ int count_part(Word& w, unsigned long long t
   }
 }
 
-// What the walk goes by.
+// What the walk goes by.  (Lengths are read again at each sequence.  Should they
+// change during the launch, the results are undefined, but the walk ends, in
+// sequences and head units that exist.)
 struct Work {
   const Cache* c;
   const int* lens;
@@ -161,8 +164,9 @@ __host__ __device__ __forceinline__ Walk start_walk_at(const Work& k, int before
   if (w.at < w.end) {
     enter_sequence(k, w);
     const long long into = w.at - (long long)before * k.HU;
-    w.hu = (int)quotient(into, w.nblk);
+    w.hu = w.nblk > 0 ? (int)quotient(into, w.nblk) : k.HU;
     w.blk = (int)(into - (long long)w.hu * w.nblk);
+    if (w.hu >= k.HU) w.at = w.end;  // the length is another by now
   }
   return w;
 }
@@ -189,11 +193,14 @@ __host__ __device__ __forceinline__ void next_unit(const Work& k, Walk& w) {
   if (++w.hu < k.HU) return;
   w.hu = 0;
   if (w.at >= w.end) return;
+  if (w.b + 1 >= k.B) return;  // (the lengths are others by now: the last sequence again)
   do {  // at < end <= total: a sequence with blocks is ahead
     ++w.b;
     enter_sequence(k, w);
   } while (w.nblk == 0 && w.b + 1 < k.B);
 }
+// Whether the walk has a unit, or a part of one, at hand.
+__host__ __device__ __forceinline__ bool at_hand(const Walk& w) { return w.at < w.end && w.nblk > 0; }
 
 // Whole units only: a CTA takes the units that begin in its share.  w: its walk;
 // next: the walk that the next CTA starts with.
