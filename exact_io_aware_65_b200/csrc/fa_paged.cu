@@ -174,10 +174,8 @@ __global__ void __launch_bounds__(APPEND_THREADS) append_kernel(const AppendPara
 // with most lanes of a warp, and its additions go to shared memory one by one
 // without waiting for each other (8 bits at a time needed the lanes of equal
 // digit matched first: 38.7 us against 13, then, for 64 heads of 7000-8192 keys).
-constexpr int SEL_THREADS = 1024;
 constexpr int SEL_SMEM_KEYS = 48 * 1024;  // 192 KB
 constexpr int SEL_BINS = 2048;
-constexpr int SEL_ROWS = 4;  // rows of K and V that a lane has on their way, in a CTA of 1024 threads
 
 struct EvictParams {
   Cache c;         // source rows
@@ -570,12 +568,8 @@ fa_status launch_paged_evict(const PagedCache& c, const Evict& e, cudaStream_t s
     constexpr int W = decltype(width)::value;
     static std::atomic<uint64_t> done[2];
     auto kern = fused ? paged::select_kernel<W, true> : paged::select_kernel<W, false>;
-    // SMs without a selection move rows meanwhile: 256 KB read and written by
-    // each, which takes about as long (eight caches of 7000-8192 rows: 37.4 us
-    // without them, 34.3 with, then)
-    const int heads = c.B * c.Hkv, idle = fused ? 0 : num_sms() - heads;
-    const long long fit = idle * (256LL << 10) / ((long long)heads * 4 * W);
-    p.early = (int)(fit < e.recent ? fit : e.recent);
+    const int heads = c.B * c.Hkv, idle = num_sms() - heads;
+    p.early = fused ? 0 : paged::early_most(heads, idle, e.recent, W);
     if (!allow_smem(done[fused], (const void*)kern, 4 * paged::SEL_SMEM_KEYS) ||
         !launch(kern, (unsigned)(heads + (p.early > 0 ? idle : 0)), paged::SEL_THREADS, smem, s, p))
       return false;

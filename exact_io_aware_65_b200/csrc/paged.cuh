@@ -215,6 +215,22 @@ __host__ __device__ __forceinline__ Walk whole_units(const Work& k, Walk w, cons
   return w;
 }
 
+// ------------------------------------------------------------------- evict ---
+constexpr int SEL_THREADS = 1024;  // of a selecting CTA
+constexpr int SEL_ROWS = 4;        // rows of K and V that a lane has on their way in one
+
+// SMs without a selection (idle, next to one for each of `heads` (sequence, head)s)
+// move rows meanwhile that need none: of each head this many at most, 256 KB read and
+// written by each SM, which takes about as long as the selection.  Not where an SM
+// would go through more than two heads, since it waits for the rows of each in turn.
+// 64 heads of 4000-8192 rows: 32.6 us without, 30.3 with; 96: 45.0, 42.7; 112: 50.4,
+// 50.6; 128: 56.6, 60.6; 144: 62, 114; 147: 63, 352.
+__host__ __device__ __forceinline__ int early_most(int heads, int idle, int recent, int row_bytes) {
+  if (heads > 2 * idle) return 0;
+  const long long fit = idle * (256LL << 10) / ((long long)heads * 4 * row_bytes);
+  return (int)(fit < recent ? fit : recent);
+}
+
 }  // namespace paged
 
 inline paged::Cache cache_view(const PagedCache& c) {
