@@ -558,12 +558,14 @@ fa_status launch_paged_evict(const PagedCache& c, const Evict& e, cudaStream_t s
   const long long most = (long long)c.max_pages * c.page_size - e.recent;
   const int smem = 4 * (int)(most < 0 ? 0 : most < paged::SEL_SMEM_KEYS ? (most + 3) / 4 * 4 : paged::SEL_SMEM_KEYS);
   // A CTA moves the rows it has selected where that is little (sequences
-  // of 500 and 1000 rows cut to 250: 10.3 against 13.3 us), or where there
-  // is a CTA for every SM; else a second kernel moves them with all SMs (eight
-  // caches of 7000-8192 rows cut to 2048: 64 CTAs alone would move 2 MB each).
+  // of 500 and 1000 rows cut to 250: 10.3 against 13.3 us); else a second kernel
+  // moves them with all SMs, also where every SM has a CTA: a selecting CTA fills its
+  // SM, and the last ones then moved alone (caches of 4000-8192 rows cut to 2048,
+  // 152 heads: 70 us, 91 in the selecting CTAs; 200: 87, 93; 256: 105, 107; 320: 132,
+  // 146; of 900-1800 rows cut to 450, 256 heads: 33, 32).
   const int rowb = c.d * c.elem;
   const long long rows = most + e.recent < e.budget ? most + e.recent : e.budget;
-  const bool fused = c.B * c.Hkv >= num_sms() || 4 * rows * rowb <= 256 * 1024;
+  const bool fused = 4 * rows * rowb <= 256 * 1024;
   auto run = [&](auto width) -> bool {
     constexpr int W = decltype(width)::value;
     static std::atomic<uint64_t> done[2];

@@ -59,3 +59,37 @@ def test_decode_of_a_serving_batch(case, e4m3):
     behind = torch.arange(cap)[None] >= torch.tensor(lens)[:, None]
     for x in (W, A):
         assert torch.equal(x.cpu().transpose(1, 2)[behind], base.transpose(1, 2)[behind])
+
+
+@pytest.mark.parametrize("B,Hkv,recent", [(21, 7, 40), (37, 4, 0), (20, 8, 300), (50, 6, 64)],
+                         ids=["147 heads", "148 heads", "160 heads", "300 heads"])
+def test_eviction_with_a_head_for_every_sm(B, Hkv, recent):
+    # rows enough for a second kernel to move them
+    budget, page, d = 300, 24, 128
+    r = random.Random(B)
+    lens = [0, 1, budget, budget + 1, 299] + [r.randint(1, 900) for _ in range(B - 5)]
+    left = [min(n, budget) for n in lens]
+    c = ref.make_cache(lens, Hkv, d, page, seed=B, extra_pages=sum(-(-n // page) for n in left) + 2, poison=False)
+    w = torch.rand((B, Hkv, c["table"].shape[1] * page), generator=torch.Generator().manual_seed(7))
+    w = (w * 50).floor() / 50  # many equal ones
+    table_out = torch.full((B, -(-budget // page)), -1, dtype=torch.int32)
+    free = list(c["free"])
+    for b, n in enumerate(left):
+        for i in range(-(-n // page)):
+            table_out[b, i] = free.pop()
+    dv = ref.dev(c)
+    wo = torch.full((B, Hkv, budget + 5), 3.0, device="cuda")
+    kept, n_out = fa.paged_evict(w.cuda(), dv["kc"], dv["vc"], dv["table"], dv["lens"], table_out.cuda(), budget, recent, wo)
+    assert fa.device_status() == 0 and n_out.tolist() == left
+    kept, wo = kept.cpu(), wo.cpu()
+    want = [c["kc"].clone(), c["vc"].clone()]
+    for b in range(B):
+        for h in range(Hkv):
+            k = ref.evict(w[b, h].tolist(), lens[b], budget, recent)
+            assert kept[b, h].tolist() == k + [-1] * (budget - len(k)), (b, h)
+            assert torch.equal(wo[b, h, :len(k)], w[b, h, k]) and not wo[b, h, len(k):].any()
+            at, frm = torch.arange(len(k)), torch.tensor(k, dtype=torch.long)
+            for pool in want:
+                pool[table_out[b, at // page].long(), h, at % page] = pool[c["table"][b, frm // page].long(), h, frm % page]
+    for got, x in ((dv["kc"], want[0]), (dv["vc"], want[1])):
+        assert torch.equal(bits(got.cpu()), bits(x))
