@@ -32,8 +32,9 @@
 // item is a key tile of a key head, and goes through the query tiles of all of
 // the head's query heads, so that the sums over them stay in tensor memory.
 // What bounds it: as in the padded form the softmax's chain from S to dS, one
-// step after the other (6100 + 8192 tokens, 16 over 4 heads of 128, causal: main
-// 1.08 ms, 985 TFLOP/s), and HBM in the other two kernels (38 and 59 us there).
+// step after the other (6100 + 8192 tokens, 16 over 4 heads of 128, causal: 1.32 ms
+// in all; main alone 1.08 ms, 985 TFLOP/s), and HBM in the other two kernels (38 and
+// 59 us there).
 //
 // CTA roles (512 threads): warp 0 TMA producer; warp 1 MMA issuer; warps
 // 4..11 softmax (thread = key row; warps 4..7 take query columns 0..63,

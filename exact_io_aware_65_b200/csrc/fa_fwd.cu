@@ -48,8 +48,9 @@
 // that share their keys, where a key head has an even number of query heads.
 // What bounds it: the softmax warps, as in the padded form, and about two key
 // tiles' time before and after an item.  6100 + 8192 tokens, 16 over 4 heads of
-// 128, causal: 385-405 us, 1060-1110 TFLOP/s; eight prompt chunks of 200-2048 tokens,
-// 32 over 8 heads: 135 us on cool clocks, 173 in a long run.
+// 128, causal: 415 us, 1030 TFLOP/s; eight prompt chunks of 200-2048 tokens, 32 over
+// 8 heads: 181 us, 780 TFLOP/s (both with the card under load, at its power limit;
+// 352 and 162 us on cool clocks).
 // SPLIT: the key tiles of an item are divided into parts, each an item of its own
 // that leaves its unnormalised O, m and l; join_kernel joins them.
 #include <cuda_bf16.h>

@@ -8,10 +8,10 @@
 // x / scale, ties to even, magnitudes above the type's largest (448) held
 // there.  Bound by the conversion's instructions (8476 tokens of 8 heads of 128
 // into 8 bits: 14.4 us, of which HBM needs 8) or by the chain of dependent loads
-// that finds the row (a step of 64 sequences: 3 us, most of it the launch).
+// that finds the row (a step of 64 sequences: 2.2 us in a graph, most of it the launch).
 // Evict.  Bound by the chain of its passes (small caches: 8 us) or by HBM (eight
-// caches of 7000-8192 rows cut to 2048, 137 MB read and written: 31 us in a graph,
-// the selection's 11 of them with an eighth of the moves beside it).
+// caches of 7000-8192 rows cut to 2048, 137 MB read and written: 36 us, 30 in a
+// graph, the selection's 11 of them with an eighth of the moves beside it).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <limits.h>
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 1) select_kernel(const EvictParam
 
 // The other rows: p.chunks blocks a (sequence, head).  Eight blocks on an SM with two
 // rows a lane: one block's chain of positions and pages hides behind the others'
-// rows (four rows a lane and four blocks: 34.3 us for the call's 30.9).
+// rows (four rows a lane and four blocks: 34.3 us for the call's 30.9, then).
 constexpr int MOVE_THREADS = 256, MOVE_ROWS = 2;
 template <int ROWB>
 __global__ void __launch_bounds__(MOVE_THREADS, 8) move_kernel(const EvictParams p) {

@@ -4,9 +4,9 @@
 // For query head h of sequence b, over the keys j < lens[b] of key head
 // h / G (G = Hq / Hkv):  s_j = scale q . k_j,  O = sum_j 2^(s_j - m) v_j / l with
 // the running maximum m and sum l of an online softmax (in log2 units), and
-// LSE = (m + log2 l) ln 2.  A key is used by G query heads and read once: the
-// call is bound by the read of the cache, 4 Nk d bytes a key head in bf16 and
-// half of that in 8 bits.
+// LSE = (m + log2 l) ln 2.  A key is used by G query heads and read once for each 16
+// of them (a unit): up to G = 16 the call is bound by one read of the cache, 4 Nk d
+// bytes a key head in bf16 and half of that in 8 bits.
 //
 // Kernel 1 (partial).  One CTA per SM; every CTA takes the same number of
 // 128-key blocks of the batch, in order, whatever sequences they belong to
@@ -29,7 +29,7 @@
 // At the end of a unit the eight warps join their (O, m, l) in shared memory;
 // a unit that lies in one CTA is finished there, a part of one goes to the
 // workspace, and the CTA that brings a unit's last part joins its parts, in their
-// order (the same bits each run): a second kernel for that cost 4 us more (one
+// order (the same bits each run): a second kernel for that cost 2 us more (one
 // sequence of 777 keys, 32 over 8 heads: 14.4 us against 12.4, then; now 10.3).
 // What it comes to: 4 sequences of 30001-32768 keys, 8 key heads of 128, in 8 bits
 // 55 us, 4.6 TB/s (bound by the instructions that widen 8 bits); the same in bf16
@@ -861,7 +861,7 @@ fa_status launch_paged_decode(const PagedCache& c, const PagedDecode& a, cudaStr
   p.R = p.G <= 8 ? 8 : 16;
   p.HB = (p.G + p.R - 1) / p.R;
   p.page = paged::make_divider(c.page_size);
-  // Short caches: a unit's few blocks one after the other take less time than
+  // Short caches (by the width of the page table): a unit's few blocks one after the other take less time than
   // their parts' join (16 sequences of 500 keys, 32 over 8 heads of 128: 10.2
   // against 16.5 us; 64 of 250, 16 heads: 35.0 against 42.1; one of 500: 9.9
   // against 9.4).

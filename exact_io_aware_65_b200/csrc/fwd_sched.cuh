@@ -42,7 +42,7 @@ struct Params {
 };
 
 // What the packed launches have besides.  (Of its own type: with these fields in
-// Params, nvcc spilled other registers of the fixed-size kernels, which took 3%
+// Params, nvcc spilled other registers of the fixed-size kernels, which took 4%
 // longer at d = 128 for it.)
 struct PackedParams : Params {
   Pack pk;
